@@ -238,6 +238,106 @@ dspark_status dspark_advance_anchor(const int32_t* out_tokens, const int32_t* n_
                                     dspark_stream_t stream);
 
 /*
+ * ------------------------------------------------------------------------
+ * Scores of given tokens, and the embedding rows of the sequential head.
+ * What a server answers with next to the tokens of a round (their log
+ * probabilities under the target, the alternatives), and what an online
+ * gradient step on the head's factors needs. The pages give no equations for
+ * either; [QbitAI] section "online drafter calibration" (the drafter corrects
+ * itself from the workload it sees) is their place in the method.
+ *
+ * These entry points take any V from 1 to 2^24 (no multiple of 8), rows of
+ * logits `row_stride` >= V elements apart (so that rows need not be 16-byte
+ * aligned; the base pointers are), and zero items (DSPARK_OK, nothing is
+ * launched). A token id of -1 marks an item to leave out. The workspace is
+ * used for its error word (except by dspark_embed_grad): any initialised
+ * workspace of dspark_workspace_bytes serves. A token id below -1 or >= V, or
+ * a row outside [0, n_rows), is recorded there (detail 0x7.......: the item)
+ * and the item treated as left out.
+ */
+
+/*
+ * Log probabilities of given tokens, entropy, and top alternatives.
+ * Item (b,c), c < C, scores tokens[b,c] on row R = row_start[b] + c of
+ * `logits` (row_start NULL: R = b*C + c), i.e. on a round's target rows with
+ * dspark_verify's out_tokens (C = K+1; -1 behind the emitted tokens):
+ *   m = max_v x_v,  s = sum_v e^(x_v - m)
+ *   logprob = x_t - m - ln s
+ *   entropy = -sum_v p_v ln p_v,  p_v = e^(x_v - m) / s  (0 ln 0 = 0)
+ *   alternatives: the top_k largest x_v in descending order, equal ones by
+ *   the lowest v (-0 equals 0), with their log probabilities.
+ * A logit of -inf is a masked token: its probability is 0, its log
+ * probability -inf, and it is no alternative. A row with nothing but -inf
+ * has logprob -inf, entropy 0, m = -inf, s = 0. A row that holds a NaN or
+ * +inf has NaN for logprob, entropy, m, s and the alternatives' log
+ * probabilities; the alternatives themselves are ranked with NaN as -inf.
+ *
+ * logits: n_rows rows of `dtype`, row_stride elements apart; row_start [B]
+ * i64 or NULL; tokens [B,C] i32; B*C <= 2^24; 0 <= top_k <= 32.
+ * Outputs: logprob [B,C] f32; entropy [B,C] f32 (may be NULL); stats [B,C,2]
+ * f32 (m, s), what dspark_logprobs_grad takes (may be NULL); top_tokens
+ * [B,C,top_k] i32 and top_logprobs [B,C,top_k] f32 (NULL with top_k = 0),
+ * -1 and -inf where a row has fewer than top_k unmasked tokens. An item left
+ * out gets 0 in logprob, entropy and stats, -1 and -inf as alternatives, and
+ * its row is not read. Sums are taken in fp32 over at most 64 terms at a time
+ * and beyond that in fp64, in an order that depends on the sizes only.
+ */
+#define DSPARK_MAX_TOP_K 32
+dspark_status dspark_logprobs(const void* logits, dspark_dtype dtype, int64_t n_rows, int64_t row_stride,
+                              const int64_t* row_start, const int32_t* tokens, int B, int C, int V, int top_k,
+                              float* logprob, float* entropy, float* stats, int32_t* top_tokens,
+                              float* top_logprobs, void* workspace, size_t ws_bytes, dspark_stream_t stream);
+
+/*
+ * Gradient of dspark_logprobs' logprob and entropy with respect to the logits
+ * (dense items: item i is row i):
+ *   dlogits[i,v] = g_logprob[i] ([v = t_i] - p_v) - g_entropy[i] p_v (ln p_v + entropy[i])
+ * with p_v from the forward call's stats. Masked logits (-inf) get 0, so does
+ * a row left out or with nothing but masked tokens; a row whose stats are NaN
+ * gets NaN. The alternatives carry no gradient.
+ *
+ * logits [N rows, row_stride apart], tokens [N] i32, stats [N,2] f32 and
+ * entropy [N] f32 as dspark_logprobs wrote them, g_logprob [N] f32,
+ * g_entropy [N] f32 or NULL (then entropy may be NULL too). Output: dlogits,
+ * N rows of the logits' dtype, grad_stride >= V elements apart (elements
+ * behind a row's V are left as they were); it may be `logits` itself with the
+ * same stride, and must not overlap it otherwise. N <= 2^24.
+ */
+dspark_status dspark_logprobs_grad(const void* logits, dspark_dtype dtype, int64_t row_stride,
+                                   const int32_t* tokens, const float* stats, const float* entropy,
+                                   const float* g_logprob, const float* g_entropy, int N, int V, void* dlogits,
+                                   int64_t grad_stride, void* workspace, size_t ws_bytes, dspark_stream_t stream);
+
+/*
+ * Embedding lookup with scaling: out[i,:] = scale * table[tokens[i],:], the
+ * product in fp32, rounded once to out's type; zeros for a token of -1.
+ * table [V,r] and out [n,r], each f32 or bf16; tokens [n] i32; 1 <= r <= 8192,
+ * n <= 2^24.
+ */
+#define DSPARK_MAX_EMBED_R 8192
+dspark_status dspark_embed(const void* table, dspark_dtype table_dtype, const int32_t* tokens, int n, int V, int r,
+                           float scale, void* out, dspark_dtype out_dtype, void* workspace, size_t ws_bytes,
+                           dspark_stream_t stream);
+
+/*
+ * Gradient of dspark_embed with respect to the table, by sorted tokens:
+ *   g_v = scale * sum_{i : tokens[i] = v} dout[i,:]
+ * dtable[v,:] = g_v for every v of [0,V) (accumulate = 0; zeros where no token
+ * points), or dtable[v,:] += g_v (accumulate = 1; rows without a token are
+ * neither read nor written). Sums are fp32 in an order that depends on the
+ * tokens and sizes only (the same call gives the same bits), rounded once to
+ * dtable's type; items with token -1 are left out.
+ * dout [n,r] and dtable [V,r], each f32 or bf16; limits as dspark_embed.
+ * The workspace holds the error word and the sorted tokens: at least
+ * dspark_embed_grad_workspace_bytes(n, V, r) bytes (0: sizes out of range),
+ * initialised once.
+ */
+size_t dspark_embed_grad_workspace_bytes(int n, int V, int r);
+dspark_status dspark_embed_grad(const void* dout, dspark_dtype dout_dtype, const int32_t* tokens, int n, int V, int r,
+                                float scale, int accumulate, void* dtable, dspark_dtype dtable_dtype,
+                                void* workspace, size_t ws_bytes, dspark_stream_t stream);
+
+/*
  * dspark_schedule without a workspace, for callers that cannot allocate
  * device memory (their allocator belongs to another framework, they run inside
  * stream capture, or their hot path forbids cudaMalloc). The pages describe no

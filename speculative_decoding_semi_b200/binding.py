@@ -64,6 +64,17 @@ def _load() -> ctypes.CDLL:
     lib.dspark_calibrate.restype = I
     lib.dspark_advance_anchor.argtypes = [P, P, I, I, P, P, Z, S]
     lib.dspark_advance_anchor.restype = I
+    L = ctypes.c_int64
+    lib.dspark_logprobs.argtypes = [P, I, L, L, P, P, I, I, I, I, P, P, P, P, P, P, Z, S]
+    lib.dspark_logprobs.restype = I
+    lib.dspark_logprobs_grad.argtypes = [P, I, L, P, P, P, P, P, I, I, P, L, P, Z, S]
+    lib.dspark_logprobs_grad.restype = I
+    lib.dspark_embed.argtypes = [P, I, P, I, I, I, F, P, I, P, Z, S]
+    lib.dspark_embed.restype = I
+    lib.dspark_embed_grad_workspace_bytes.argtypes = [I, I, I]
+    lib.dspark_embed_grad_workspace_bytes.restype = Z
+    lib.dspark_embed_grad.argtypes = [P, I, P, I, I, I, F, I, P, I, P, Z, S]
+    lib.dspark_embed_grad.restype = I
     lib.dspark_set_wait_budget.argtypes = [P, ctypes.c_uint32, S]
     lib.dspark_set_wait_budget.restype = I
     lib.dspark_inject_stall.argtypes = [P, I, ctypes.c_uint32, S]
@@ -272,6 +283,128 @@ def dspark_advance_anchor(out_tokens, n_out, anchor, workspace, stream=None) -> 
         _ptr(anchor, "anchor", torch.int32, B), _ptr(workspace, "workspace", torch.uint8), workspace.numel(),
         _stream(stream))
     _check("dspark_advance_anchor", st)
+
+
+DSPARK_MAX_TOP_K, DSPARK_MAX_EMBED_R = 32, 8192
+_DTYPES = {torch.float32: DSPARK_F32, torch.bfloat16: DSPARK_BF16}
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _rows(t: torch.Tensor, name: str) -> tuple[int, int, int, int]:
+    """(pointer, rows, columns, row stride) of a [rows, columns] CUDA tensor
+    whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor (the library computes on the GPU only)")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected two dimensions, got {t.dim()}")
+    rows, cols = t.shape
+    stride = t.stride(0) if rows > 1 else cols
+    if cols > 1 and t.stride(1) != 1 or stride < cols:
+        raise ValueError(f"{name}: expected contiguous rows at least {cols} elements apart")
+    return t.data_ptr(), rows, cols, stride
+
+
+def _on_device(fn: str, first: torch.Tensor, tensors, stream, call) -> None:
+    """Make the call with the tensors' device current, so that the launch and
+    the default stream are that device's; all of them have to be on it."""
+    dev = first.device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{fn}: tensors on {dev} and {t.device}")
+    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+        raise ValueError(f"{fn}: tensors on {dev}, stream on {stream.device}")
+    if dev.index == torch.cuda.current_device():
+        _check(fn, call(_stream(stream)))
+        return
+    with torch.cuda.device(dev):
+        _check(fn, call(_stream(stream)))
+
+
+def dspark_logprobs(logits, tokens, logprob, entropy, stats, top_tokens, top_logprobs, workspace, row_start=None,
+                    stream=None) -> None:
+    """Log probabilities of tokens [B,C] (-1: left out) on rows of logits
+    [rows,V] (float32 or bfloat16, rows any stride apart): row row_start[b] + c,
+    or b*C + c without row_start. entropy, stats and (both) alternatives may be
+    None; top_k is their last dimension."""
+    dt = _dtype(logits, "logits")
+    ptr, n_rows, V, ld = _rows(logits, "logits")
+    B, C = tokens.shape
+    n = B * C
+    if (top_tokens is None) != (top_logprobs is None):
+        raise ValueError("top_tokens and top_logprobs: give both or neither")
+    k = 0
+    if top_tokens is not None:
+        if top_tokens.dim() != 3:
+            raise ValueError("top_tokens: expected [B,C,top_k]")
+        k = top_tokens.shape[-1]
+    args = (ptr, dt, n_rows, ld, _ptr(row_start, "row_start", torch.int64, B), _ptr(tokens, "tokens", torch.int32),
+            B, C, V, k, _ptr(logprob, "logprob", torch.float32, n), _ptr(entropy, "entropy", torch.float32, n),
+            _ptr(stats, "stats", torch.float32, 2 * n), _ptr(top_tokens, "top_tokens", torch.int32, n * k),
+            _ptr(top_logprobs, "top_logprobs", torch.float32, n * k), _ptr(workspace, "workspace", torch.uint8),
+            workspace.numel())
+    _on_device("dspark_logprobs", logits,
+               (tokens, logprob, entropy, stats, top_tokens, top_logprobs, workspace, row_start), stream,
+               lambda s: lib.dspark_logprobs(*args, s))
+
+
+def dspark_logprobs_grad(logits, tokens, stats, entropy, g_logprob, g_entropy, dlogits, workspace,
+                         stream=None) -> None:
+    """dlogits [N,V] = the gradient of dspark_logprobs' logprob (times
+    g_logprob [N]) and entropy (times g_entropy [N], or None) with respect to
+    logits [N,V]; tokens [N] or any shape of N elements. dlogits may be logits."""
+    dt = _dtype(logits, "logits")
+    if _dtype(dlogits, "dlogits") != dt:
+        raise TypeError("dlogits: expected the type of logits")
+    ptr, N, V, ld = _rows(logits, "logits")
+    gptr, gN, gV, gld = _rows(dlogits, "dlogits")
+    if (gN, gV) != (N, V):
+        raise ValueError(f"dlogits: expected [{N},{V}], got [{gN},{gV}]")
+    if g_entropy is not None and entropy is None:
+        raise ValueError("entropy: needed with g_entropy")
+    args = (ptr, dt, ld, _ptr(tokens, "tokens", torch.int32, N), _ptr(stats, "stats", torch.float32, 2 * N),
+            _ptr(entropy, "entropy", torch.float32, N), _ptr(g_logprob, "g_logprob", torch.float32, N),
+            _ptr(g_entropy, "g_entropy", torch.float32, N), N, V, gptr, gld,
+            _ptr(workspace, "workspace", torch.uint8), workspace.numel())
+    _on_device("dspark_logprobs_grad", logits,
+               (tokens, stats, entropy, g_logprob, g_entropy, dlogits, workspace), stream,
+               lambda s: lib.dspark_logprobs_grad(*args, s))
+
+
+def dspark_embed(table, tokens, scale: float, out, workspace, stream=None) -> None:
+    """out [n,r] = scale * table[tokens] (zeros for a token of -1); table [V,r]
+    and out each float32 or bfloat16."""
+    V, r = table.shape
+    n = tokens.numel()
+    args = (_ptr(table, "table"), _dtype(table, "table"), _ptr(tokens, "tokens", torch.int32), n, V, r, float(scale),
+            _ptr(out, "out", numel=n * r), _dtype(out, "out"), _ptr(workspace, "workspace", torch.uint8),
+            workspace.numel())
+    _on_device("dspark_embed", table, (tokens, out, workspace), stream, lambda s: lib.dspark_embed(*args, s))
+
+
+def dspark_embed_grad_workspace_bytes(n: int, V: int, r: int) -> int:
+    size = lib.dspark_embed_grad_workspace_bytes(n, V, r)
+    if size == 0:
+        raise DSparkError("dspark_embed_grad_workspace_bytes", 1)
+    return int(size)
+
+
+def dspark_embed_grad(dout, tokens, scale: float, dtable, workspace, accumulate: bool = False, stream=None) -> None:
+    """dtable [V,r] = (accumulate: +=) scale * the sum of dout's rows [n,r] over
+    the items of each token; dout and dtable each float32 or bfloat16."""
+    V, r = dtable.shape
+    n = tokens.numel()
+    args = (_ptr(dout, "dout", numel=n * r), _dtype(dout, "dout"), _ptr(tokens, "tokens", torch.int32), n, V, r,
+            float(scale), int(bool(accumulate)), _ptr(dtable, "dtable"), _dtype(dtable, "dtable"),
+            _ptr(workspace, "workspace", torch.uint8), workspace.numel())
+    _on_device("dspark_embed_grad", dtable, (dout, tokens, workspace), stream,
+               lambda s: lib.dspark_embed_grad(*args, s))
 
 
 DSPARK_INJECT_NONE, DSPARK_INJECT_DRAFT_SLICE_SUMS, DSPARK_INJECT_VERIFY_BARRIER = 0, 1, 2
