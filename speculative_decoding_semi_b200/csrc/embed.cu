@@ -1,4 +1,5 @@
-// Embedding lookup with scaling, and its gradient with respect to the table.
+// Embedding lookup with scaling, and its gradient with respect to the table
+// by sorted tokens.
 #include <algorithm>
 
 #include "common.cuh"
@@ -7,7 +8,25 @@ namespace dspark {
 namespace {
 
 constexpr int kMaxItems = 1 << 24;
-constexpr int kThreads = 256;
+constexpr int kMaxSms = 148;   // owners of table rows, one CTA each (more only for very large V)
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(uint16_t x) { return bf16_bits_to_float(x); }
+
+// Two fp32 values as a pair of bf16, rounded to nearest even.
+__device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
+  unsigned r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void store(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store(uint16_t* p, float v) { *p = static_cast<uint16_t>(pack_bf16(v, 0.f)); }
+
+__device__ __forceinline__ void record_bad_token(unsigned* err, int item) {
+  set_error(err, DSPARK_ERR_DEVICE_ASSERT, 0x70000000u | static_cast<unsigned>(item));
+}
+
+// ---------------------------------------------------------------- lookup
 
 struct EmbedArgs {
   const void* table;
@@ -18,23 +37,7 @@ struct EmbedArgs {
   unsigned* err;
 };
 
-struct EmbedGradArgs {
-  const void* dout;
-  const int32_t* tokens;
-  int n, V, r;
-  float scale;
-  int accumulate;
-  void* dtable;
-  unsigned* err;
-};
-
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(uint16_t x) { return bf16_bits_to_float(x); }
-
-__device__ __forceinline__ void store(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store(uint16_t* p, float v) {
-  asm volatile("{ .reg .b16 h; cvt.rn.bf16.f32 h, %1; st.global.b16 [%0], h; }" ::"l"(p), "f"(v) : "memory");
-}
+constexpr int kThreads = 256;
 
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a) {
@@ -42,39 +45,424 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a) {
   const int t = a.tokens[i];
   TO* out = static_cast<TO*>(a.out) + static_cast<long long>(i) * a.r;
   const bool ok = t >= 0 && t < a.V;
-  if (!ok && t != -1 && threadIdx.x == 0)
-    set_error(a.err, DSPARK_ERR_DEVICE_ASSERT, 0x70000000u | static_cast<unsigned>(i));
+  if (!ok && t != -1 && threadIdx.x == 0) record_bad_token(a.err, i);
   const TI* row = static_cast<const TI*>(a.table) + static_cast<long long>(ok ? t : 0) * a.r;
   for (int k = threadIdx.x; k < a.r; k += kThreads) store(out + k, ok ? to_float(row[k]) * a.scale : 0.f);
 }
 
+// -------------------------------------------------------------- gradient
+//
+// dtable[v] = scale * sum of dout's rows whose token is v. Two kernels:
+//
+// sort_kernel: CTA g owns table rows [g R, (g+1) R). It reads all n tokens,
+//   counts those below its rows (its offset in the sorted order, so the CTAs
+//   need not talk to each other) and counting-sorts its own, stably: each of
+//   16 warps takes a contiguous piece of the tokens, keeps its matches in
+//   order, counts them per row, and places them after the earlier warps'.
+//   It then zeroes its rows that no token points at.
+// sum_kernel: the sorted items in equal pieces, whatever the lengths of the
+//   runs of equal tokens, so that a frequent token is summed by many CTAs. A
+//   run inside a piece is written at once; the parts of a run that crosses
+//   pieces go to scratch, and the CTA that delivers the last part (a counter)
+//   adds them in order. Which CTA that is does not change the order.
+//
+// Few items with accumulate: direct_kernel, one CTA an item, no sorting.
+
+struct GradArgs {
+  const void* dout;
+  const int32_t* tokens;
+  int n, V, r;
+  float scale;
+  int accumulate;
+  void* dtable;
+  unsigned* err;
+  int R, slabs, pieces;   // table rows of an owner; 128-column slabs; pieces of the sorted items
+  int* n_sorted;          // items with a token
+  unsigned* arrived;      // [pieces][slabs] parts of the run that starts in a piece and leaves it
+  int4* sorted;           // [n] item, token, and the run [begin, end) it is in
+  float* parts;           // [pieces][2][slabs * 128]: of the run that comes in, of the run that leaves
+};
+
+constexpr int kSortWarps = 16, kSortThreads = kSortWarps * 32;
+constexpr int kMaxR = 2048;     // rows of an owner (11 bits beside 20 of an item's place in a warp's piece)
+constexpr int kKeep = 512;      // matches that a warp keeps in shared memory; more are found again
+constexpr int kSumWarps = 8, kSumThreads = kSumWarps * 32;
+constexpr int kSlab = 128;      // columns of a warp: four a lane
+constexpr int kDirectItems = 1024;
+constexpr int kDirectThreads = 128;
+
+__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
 template <typename TO>
-__global__ void __launch_bounds__(kThreads) zero_kernel(EmbedGradArgs a) {
-  TO* d = static_cast<TO*>(a.dtable) + static_cast<long long>(blockIdx.x) * a.r;
-  for (int k = threadIdx.x; k < a.r; k += kThreads) store(d + k, 0.f);
+__device__ __forceinline__ void zero_row(TO* d, int r, int lane) {
+  const int bytes = r * static_cast<int>(sizeof(TO));
+  if (bytes % 16 == 0) {
+    for (int k = lane; k < bytes / 16; k += 32) reinterpret_cast<uint4*>(d)[k] = make_uint4(0, 0, 0, 0);
+  } else {
+    for (int k = lane; k < r; k += 32) store(d + k, 0.f);
+  }
 }
 
-// One CTA an item; the CTA of a token's first item sums all of that token's
-// items in order.
-template <typename TI, typename TO>
-__global__ void __launch_bounds__(kThreads) embed_grad_kernel(EmbedGradArgs a) {
-  const int i = blockIdx.x, tid = threadIdx.x;
+template <typename TO>
+__global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(GradArgs a) {
+  extern __shared__ unsigned smem[];
+  unsigned* hist = smem;                                   // [16][R] counts, then places
+  unsigned* total = hist + kSortWarps * a.R;               // [R] tokens of a row
+  unsigned* kept = total + a.R;                            // [16][kKeep]
+  __shared__ unsigned s_below, s_red[kSortWarps];
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, R = a.R, n = a.n;
+  const int v0 = blockIdx.x * R, rows = min(R, a.V - v0);
+  const unsigned lt = (1u << lane) - 1u;
+  for (int k = tid; k < kSortWarps * R; k += kSortThreads) hist[k] = 0;
+  if (tid == 0) s_below = 0;
+  for (int k = blockIdx.x * kSortThreads + tid; k < a.pieces * a.slabs; k += gridDim.x * kSortThreads) a.arrived[k] = 0;
+  __syncthreads();
+
+  // each warp's matches, in order
+  const int len = ceil_div(ceil_div(n, kSortWarps), 32) * 32;
+  const int lo = min(n, w * len), hi = min(n, lo + len);
+  unsigned* mine = kept + w * kKeep;
+  unsigned* count = hist + w * R;
+  int found = 0;
+  unsigned below = 0;
+  constexpr int kAhead = 8;
+  for (int i0 = lo; i0 < hi; i0 += 32 * kAhead) {
+    int t[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u * 32 + lane;
+      t[u] = i < hi ? __ldg(a.tokens + i) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u * 32 + lane;
+      if (t[u] < -1 || t[u] >= a.V) {
+        if (blockIdx.x == 0) record_bad_token(a.err, i);
+        t[u] = -1;
+      }
+      below += t[u] >= 0 && t[u] < v0;
+      const unsigned off = static_cast<unsigned>(t[u] - v0);
+      const bool hit = t[u] >= 0 && off < static_cast<unsigned>(rows);
+      const unsigned mask = __ballot_sync(0xffffffffu, hit);
+      if (mask != 0u) {
+        const int at = found + __popc(mask & lt);
+        if (hit) {
+          atomicAdd(count + off, 1u);
+          if (at < kKeep) mine[at] = (static_cast<unsigned>(i - lo) << 11) | off;
+        }
+        found += __popc(mask);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
+  if (lane == 0 && below != 0u) atomicAdd(&s_below, below);
+  __syncthreads();
+
+  // places: rows in order, within a row the warps in order
+  const int per = ceil_div(rows, kSortThreads), r0 = min(rows, tid * per), r1 = min(rows, r0 + per);
+  unsigned sum = 0;
+  for (int k = r0; k < r1; ++k) {
+    unsigned c = 0;
+#pragma unroll
+    for (int j = 0; j < kSortWarps; ++j) {
+      const unsigned x = hist[j * R + k];
+      hist[j * R + k] = c;
+      c += x;
+    }
+    total[k] = c;
+    sum += c;
+  }
+  unsigned inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) s_red[w] = inc;
+  __syncthreads();
+  unsigned place = s_below + inc - sum;
+  for (int j = 0; j < w; ++j) place += s_red[j];
+  for (int k = r0; k < r1; ++k) {
+#pragma unroll
+    for (int j = 0; j < kSortWarps; ++j) hist[j * R + k] += place;
+    place += total[k];
+  }
+  if (blockIdx.x == gridDim.x - 1 && tid == kSortThreads - 1) *a.n_sorted = static_cast<int>(place);
+  __syncthreads();
+
+  auto put = [&](bool hit, unsigned off, int item) {   // by the whole warp
+    const unsigned peers = __match_any_sync(0xffffffffu, hit ? off : 0xffffffffu);
+    if (hit) {
+      const int at = static_cast<int>(count[off]) + __popc(peers & lt);
+      // the run: warp 0's first place to the last warp's end
+      a.sorted[at] = make_int4(item, v0 + static_cast<int>(off), 0, 0);
+    }
+    __syncwarp();
+    if (hit && (peers & lt) == 0u) count[off] += __popc(peers);
+    __syncwarp();
+  };
+  if (found <= kKeep) {
+    for (int k0 = 0; k0 < found; k0 += 32) {
+      const bool hit = k0 + lane < found;
+      const unsigned e = hit ? mine[k0 + lane] : 0u;
+      put(hit, e & 2047u, lo + static_cast<int>(e >> 11));
+    }
+  } else {
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+      const int i = i0 + lane, t = i < hi ? __ldg(a.tokens + i) : -1;
+      const unsigned off = static_cast<unsigned>(t - v0);
+      const bool hit = t >= 0 && off < static_cast<unsigned>(rows);
+      if (__any_sync(0xffffffffu, hit)) put(hit, off, i);
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __syncthreads();
+  // after the placement the last warp's place is each run's end
+  const unsigned* ends = hist + (kSortWarps - 1) * R;
+  for (int k = w; k < rows; k += kSortWarps) {
+    const int c = static_cast<int>(total[k]), end = static_cast<int>(ends[k]);
+    for (int j = lane; j < c; j += 32) {
+      int4* s = a.sorted + (end - c + j);
+      reinterpret_cast<int2*>(s)[1] = make_int2(end - c, end);
+    }
+    if (c == 0 && !a.accumulate) zero_row(static_cast<TO*>(a.dtable) + static_cast<long long>(v0 + k) * a.r, a.r, lane);
+  }
+}
+
+// Four columns of a row: neighbours (r a multiple of 4), or 32 apart.
+template <typename T, bool kVec>
+struct Cols;
+template <bool kVec>
+struct Cols<float, kVec> {
+  __device__ __forceinline__ static float4 load(const float* p, int lane, int cols) {
+    if (kVec) return lane * 4 < cols ? __ldcs(reinterpret_cast<const float4*>(p) + lane) : make_float4(0, 0, 0, 0);
+    float4 v;
+    v.x = lane < cols ? p[lane] : 0.f;
+    v.y = lane + 32 < cols ? p[lane + 32] : 0.f;
+    v.z = lane + 64 < cols ? p[lane + 64] : 0.f;
+    v.w = lane + 96 < cols ? p[lane + 96] : 0.f;
+    return v;
+  }
+  __device__ __forceinline__ static void save(float* p, int lane, int cols, float4 v) {
+    if (kVec) {
+      if (lane * 4 < cols) reinterpret_cast<float4*>(p)[lane] = v;
+      return;
+    }
+    if (lane < cols) p[lane] = v.x;
+    if (lane + 32 < cols) p[lane + 32] = v.y;
+    if (lane + 64 < cols) p[lane + 64] = v.z;
+    if (lane + 96 < cols) p[lane + 96] = v.w;
+  }
+};
+template <bool kVec>
+struct Cols<uint16_t, kVec> {
+  __device__ __forceinline__ static float4 load(const uint16_t* p, int lane, int cols) {
+    if (kVec) {
+      const uint2 u = lane * 4 < cols ? __ldcs(reinterpret_cast<const uint2*>(p) + lane) : make_uint2(0, 0);
+      return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                         __uint_as_float(u.y & 0xffff0000u));
+    }
+    float4 v;
+    v.x = lane < cols ? bf16_bits_to_float(p[lane]) : 0.f;
+    v.y = lane + 32 < cols ? bf16_bits_to_float(p[lane + 32]) : 0.f;
+    v.z = lane + 64 < cols ? bf16_bits_to_float(p[lane + 64]) : 0.f;
+    v.w = lane + 96 < cols ? bf16_bits_to_float(p[lane + 96]) : 0.f;
+    return v;
+  }
+  __device__ __forceinline__ static void save(uint16_t* p, int lane, int cols, float4 v) {
+    if (kVec) {
+      if (lane * 4 < cols) reinterpret_cast<uint2*>(p)[lane] = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+      return;
+    }
+    if (lane < cols) store(p + lane, v.x);
+    if (lane + 32 < cols) store(p + lane + 32, v.y);
+    if (lane + 64 < cols) store(p + lane + 64, v.z);
+    if (lane + 96 < cols) store(p + lane + 96, v.w);
+  }
+};
+
+__device__ __forceinline__ float4 plus(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
+// dtable[token, slab] (+)= scale * sum
+template <typename TO, bool kVec>
+__device__ __forceinline__ void finish(const GradArgs& a, int token, int slab, int lane, int cols, float4 s) {
+  TO* d = static_cast<TO*>(a.dtable) + static_cast<long long>(token) * a.r + slab * kSlab;
+  s = make_float4(s.x * a.scale, s.y * a.scale, s.z * a.scale, s.w * a.scale);
+  if (a.accumulate) s = plus(s, Cols<TO, kVec>::load(d, lane, cols));
+  Cols<TO, kVec>::save(d, lane, cols, s);
+}
+
+// A piece is kSumWarps * P sorted items, P a warp, on one slab.
+template <typename TI, typename TO, bool kVec, int P>
+__global__ void __launch_bounds__(kSumThreads) sum_kernel(GradArgs a) {
+  constexpr int kPiece = kSumWarps * P;
+  __shared__ float4 s_part[kSumWarps][2][32];
+  __shared__ int4 s_run[kSumWarps][2];   // token, begin, end of each part; token -1: none
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int piece = blockIdx.x / a.slabs, slab = blockIdx.x - piece * a.slabs;
+  const int N = *a.n_sorted, p0 = piece * kPiece;
+  if (p0 >= N) return;
+  const int cols = min(kSlab, a.r - slab * kSlab);
+  const TI* dout = static_cast<const TI*>(a.dout) + slab * kSlab;
+  const int lo = p0 + w * P, hi = min(N, lo + P);
+  int4 it = make_int4(0, -1, 0, 0);
+  if (lane < P && lo + lane < hi) it = a.sorted[lo + lane];
+  if (lane < 2) s_run[w][lane].x = -1;
+  __syncwarp();
+  float4 sum = make_float4(0, 0, 0, 0);
+  constexpr int kAhead = 8;
+  for (int j0 = 0; j0 < P; j0 += kAhead) {
+    if (lo + j0 >= hi) break;
+    float4 x[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int item = __shfl_sync(0xffffffffu, it.x, j0 + u);
+      x[u] = lo + j0 + u < hi ? Cols<TI, kVec>::load(dout + static_cast<long long>(item) * a.r, lane, cols)
+                              : make_float4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int j = j0 + u, pos = lo + j;
+      const int token = __shfl_sync(0xffffffffu, it.y, j);
+      const int begin = __shfl_sync(0xffffffffu, it.z, j), end = __shfl_sync(0xffffffffu, it.w, j);
+      if (pos < hi) {
+        sum = plus(sum, x[u]);
+        if (pos == end - 1 || pos == hi - 1) {      // the run, or this warp's part of it, ends here
+          if (begin >= lo && end <= hi) {
+            finish<TO, kVec>(a, token, slab, lane, cols, sum);
+          } else {
+            const int k = begin < lo ? 0 : 1;       // came in, or leaves
+            s_part[w][k][lane] = sum;
+            if (lane == 0) s_run[w][k] = make_int4(token, begin, end, 0);
+          }
+          sum = make_float4(0, 0, 0, 0);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (w != 0) return;
+  // the warps' parts in order: equal tokens are one run
+  const int piece_end = min(N, p0 + kPiece);
+  int token = -1, begin = 0, end = 0;
+  sum = make_float4(0, 0, 0, 0);
+  const long long row = static_cast<long long>(a.slabs) * kSlab;
+  auto flush = [&]() {
+    if (token < 0) return;
+    if (begin >= p0 && end <= piece_end) {
+      finish<TO, kVec>(a, token, slab, lane, cols, sum);
+      return;
+    }
+    float4* parts = reinterpret_cast<float4*>(a.parts + slab * kSlab) + lane;
+    __stcg(parts + (2ll * piece + (begin < p0 ? 0 : 1)) * (row / 4), sum);
+    const int first = begin / kPiece, last = (end - 1) / kPiece;
+    __threadfence();
+    __syncwarp();
+    unsigned before = 0;
+    if (lane == 0) before = atom_add_acq_rel_gpu(a.arrived + static_cast<long long>(first) * a.slabs + slab, 1u);
+    before = __shfl_sync(0xffffffffu, before, 0);
+    if (before != static_cast<unsigned>(last - first)) return;
+    __threadfence();
+    sum = __ldcg(parts + (2ll * first + 1) * (row / 4));
+    int q = first + 1;
+    for (; q + 8 <= last + 1; q += 8) {
+      float4 x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = __ldcg(parts + 2ll * (q + u) * (row / 4));
+#pragma unroll
+      for (int u = 0; u < 8; ++u) sum = plus(sum, x[u]);
+    }
+    for (; q <= last; ++q) sum = plus(sum, __ldcg(parts + 2ll * q * (row / 4)));
+    finish<TO, kVec>(a, token, slab, lane, cols, sum);
+  };
+  for (int j = 0; j < kSumWarps * 2; ++j) {
+    const int4 run = s_run[j >> 1][j & 1];
+    if (run.x < 0) continue;
+    if (run.x != token) {
+      flush();
+      token = run.x;
+      begin = run.y;
+      end = run.z;
+      sum = make_float4(0, 0, 0, 0);
+    }
+    sum = plus(sum, s_part[j >> 1][j & 1][lane]);
+  }
+  flush();
+}
+
+// One CTA an item and 512 columns; the CTA of a token's first item sums all of
+// that token's items in order.
+template <typename TI, typename TO, bool kVec>
+__global__ void __launch_bounds__(kDirectThreads) direct_kernel(GradArgs a) {
+  __shared__ unsigned s_hits[kDirectItems / 32];
+  const int i = blockIdx.x, tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int t = a.tokens[i];
   if (t < 0 || t >= a.V) {
-    if (t != -1 && tid == 0) set_error(a.err, DSPARK_ERR_DEVICE_ASSERT, 0x70000000u | static_cast<unsigned>(i));
+    if (t != -1 && tid == 0 && blockIdx.y == 0) record_bad_token(a.err, i);
     return;
   }
-  int before = 0;
-  for (int j = tid; j < i; j += kThreads) before |= a.tokens[j] == t;
-  if (__syncthreads_or(before)) return;
-  TO* d = static_cast<TO*>(a.dtable) + static_cast<long long>(t) * a.r;
-  for (int k0 = 0; k0 < a.r; k0 += kThreads) {
-    const int k = k0 + tid;
-    float s = 0.f;
-    for (int j = i; j < a.n; ++j)
-      if (a.tokens[j] == t && k < a.r) s += to_float(static_cast<const TI*>(a.dout)[static_cast<long long>(j) * a.r + k]);
-    if (k < a.r) store(d + k, a.accumulate ? fmaf(s, a.scale, to_float(d[k])) : s * a.scale);
+  bool before = false;
+  const int words = ceil_div(a.n, 32);
+  for (int k = w; k < words; k += kDirectThreads / 32) {
+    const int j = k * 32 + lane;
+    const bool hit = j < a.n && __ldg(a.tokens + j) == t;
+    before |= hit && j < i;
+    const unsigned mask = __ballot_sync(0xffffffffu, hit);
+    if (lane == 0) s_hits[k] = mask;
   }
+  if (__syncthreads_or(before)) return;
+  const int slab = blockIdx.y * (kDirectThreads / 32) + w;
+  if (slab >= a.slabs) return;
+  const int cols = min(kSlab, a.r - slab * kSlab);
+  const TI* dout = static_cast<const TI*>(a.dout) + slab * kSlab;
+  float4 sum = make_float4(0, 0, 0, 0);
+  for (int k = i >> 5; k < words; ++k) {
+    unsigned m = s_hits[k];
+    while (m != 0u) {
+      int item[4], c = 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (m != 0u) {
+          item[u] = k * 32 + __ffs(m) - 1;
+          m &= m - 1;
+          ++c;
+        }
+      float4 x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (u < c) x[u] = Cols<TI, kVec>::load(dout + static_cast<long long>(item[u]) * a.r, lane, cols);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (u < c) sum = plus(sum, x[u]);
+    }
+  }
+  finish<TO, kVec>(a, t, slab, lane, cols, sum);
+}
+
+// Sizes of the two-kernel path for (n, V, r), and its scratch.
+struct GradPlan {
+  int R, owners, slabs, P, pieces;
+  size_t smem, off_n, off_arrived, off_sorted, off_parts, bytes;
+};
+GradPlan grad_plan(int n, int V, int r) {
+  GradPlan p{};
+  p.R = std::min(kMaxR, ceil_div(V, kMaxSms));
+  p.owners = ceil_div(V, p.R);
+  p.slabs = ceil_div(r, kSlab);
+  // 32 items a warp where that still makes four CTAs an SM, else 8
+  p.P = static_cast<long long>(n) * p.slabs >= 4ll * kMaxSms * kSumWarps * 32 ? 32 : 8;
+  p.pieces = std::max(1, ceil_div(n, kSumWarps * p.P));
+  p.smem = static_cast<size_t>(kSortWarps * p.R + p.R + kSortWarps * kKeep) * sizeof(unsigned);
+  p.off_n = kScratchOffset;
+  p.off_arrived = p.off_n + 256;
+  p.off_sorted = align_up(p.off_arrived + static_cast<size_t>(p.pieces) * p.slabs * sizeof(unsigned), 256);
+  p.off_parts = align_up(p.off_sorted + static_cast<size_t>(n) * sizeof(int4), 256);
+  p.bytes = align_up(p.off_parts + static_cast<size_t>(p.pieces) * 2 * p.slabs * kSlab * sizeof(float), 256);
+  return p;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -82,6 +470,44 @@ bool given(const void* p) { return p != nullptr && aligned16(p); }
 bool dtype_ok(dspark_dtype t) { return t == DSPARK_F32 || t == DSPARK_BF16; }
 bool embed_sizes_ok(int n, int V, int r) {
   return n >= 0 && n <= kMaxItems && V >= 1 && V <= kMaxV && r >= 1 && r <= DSPARK_MAX_EMBED_R;
+}
+
+template <typename TI, typename TO, bool kVec>
+cudaError_t launch_grad(GradArgs a, char* ws, cudaStream_t s) {
+  const GradPlan p = grad_plan(a.n, a.V, a.r);
+  a.R = p.R;
+  a.slabs = p.slabs;
+  a.pieces = p.pieces;
+  if (a.accumulate && a.n <= kDirectItems) {
+    if (a.n > 0)
+      direct_kernel<TI, TO, kVec><<<dim3(a.n, ceil_div(p.slabs, kDirectThreads / 32)), kDirectThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  a.n_sorted = reinterpret_cast<int*>(ws + p.off_n);
+  a.arrived = reinterpret_cast<unsigned*>(ws + p.off_arrived);
+  a.sorted = reinterpret_cast<int4*>(ws + p.off_sorted);
+  a.parts = reinterpret_cast<float*>(ws + p.off_parts);
+  cudaError_t e = cudaFuncSetAttribute(sort_kernel<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(p.smem));
+  if (e != cudaSuccess) return e;
+  sort_kernel<TO><<<p.owners, kSortThreads, p.smem, s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.n == 0) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.pieces * p.slabs);
+  cfg.blockDim = dim3(kSumThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, p.P == 32 ? sum_kernel<TI, TO, kVec, 32> : sum_kernel<TI, TO, kVec, 8>, a);
+}
+
+template <typename TI, typename TO>
+cudaError_t launch_grad(const GradArgs& a, char* ws, cudaStream_t s) {
+  return a.r % 4 == 0 ? launch_grad<TI, TO, true>(a, ws, s) : launch_grad<TI, TO, false>(a, ws, s);
 }
 
 }  // namespace
@@ -109,8 +535,7 @@ dspark_status dspark_embed(const void* table, dspark_dtype table_dtype, const in
 }
 
 size_t dspark_embed_grad_workspace_bytes(int n, int V, int r) {
-  if (!embed_sizes_ok(n, V, r)) return 0;
-  return kScratchOffset;
+  return embed_sizes_ok(n, V, r) ? grad_plan(n, V, r).bytes : 0;
 }
 
 dspark_status dspark_embed_grad(const void* dout, dspark_dtype dout_dtype, const int32_t* tokens, int n, int V, int r,
@@ -121,18 +546,24 @@ dspark_status dspark_embed_grad(const void* dout, dspark_dtype dout_dtype, const
   if (!given(dtable) || !given(workspace)) return DSPARK_ERR_INVALID_ARG;
   if (n > 0 && (!given(dout) || !given(tokens))) return DSPARK_ERR_INVALID_ARG;
   if (ws_bytes < dspark_embed_grad_workspace_bytes(n, V, r)) return DSPARK_ERR_INVALID_ARG;
-  const EmbedGradArgs a{dout, tokens, n, V, r, scale, accumulate, dtable,
-                        reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + kErrOffset)};
+  GradArgs a{};
+  a.dout = dout;
+  a.tokens = tokens;
+  a.n = n;
+  a.V = V;
+  a.r = r;
+  a.scale = scale;
+  a.accumulate = accumulate;
+  a.dtable = dtable;
+  char* ws = static_cast<char*>(workspace);
+  a.err = reinterpret_cast<unsigned*>(ws + kErrOffset);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!accumulate) (dtable_dtype == DSPARK_F32 ? zero_kernel<float> : zero_kernel<uint16_t>)<<<V, kThreads, 0, s>>>(a);
-  if (n > 0) {
-    auto kernel =
-        dout_dtype == DSPARK_F32
-            ? (dtable_dtype == DSPARK_F32 ? embed_grad_kernel<float, float> : embed_grad_kernel<float, uint16_t>)
-            : (dtable_dtype == DSPARK_F32 ? embed_grad_kernel<uint16_t, float> : embed_grad_kernel<uint16_t, uint16_t>);
-    kernel<<<n, kThreads, 0, s>>>(a);
-  }
-  return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  const cudaError_t e =
+      dout_dtype == DSPARK_F32
+          ? (dtable_dtype == DSPARK_F32 ? launch_grad<float, float>(a, ws, s) : launch_grad<float, uint16_t>(a, ws, s))
+          : (dtable_dtype == DSPARK_F32 ? launch_grad<uint16_t, float>(a, ws, s)
+                                        : launch_grad<uint16_t, uint16_t>(a, ws, s));
+  return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 }  // extern "C"
