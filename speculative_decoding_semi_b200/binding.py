@@ -305,26 +305,42 @@ def _rows(t: torch.Tensor, name: str) -> tuple[int, int, int, int]:
     if t.dim() != 2:
         raise ValueError(f"{name}: expected two dimensions, got {t.dim()}")
     rows, cols = t.shape
-    stride = t.stride(0) if rows > 1 else cols
-    if cols > 1 and t.stride(1) != 1 or stride < cols:
+    if t.is_contiguous():
+        return t.data_ptr(), rows, cols, cols
+    stride, step = t.stride()
+    if cols > 1 and step != 1 or rows > 1 and stride < cols:
         raise ValueError(f"{name}: expected contiguous rows at least {cols} elements apart")
-    return t.data_ptr(), rows, cols, stride
+    return t.data_ptr(), rows, cols, max(stride, cols)
 
 
-def _on_device(fn: str, first: torch.Tensor, tensors, stream, call) -> None:
-    """Make the call with the tensors' device current, so that the launch and
-    the default stream are that device's; all of them have to be on it."""
-    dev = first.device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{fn}: tensors on {dev} and {t.device}")
-    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
-        raise ValueError(f"{fn}: tensors on {dev}, stream on {stream.device}")
-    if dev.index == torch.cuda.current_device():
-        _check(fn, call(_stream(stream)))
-        return
-    with torch.cuda.device(dev):
-        _check(fn, call(_stream(stream)))
+def _on(dev: int, t: torch.Tensor | None, name: str, dtype, numel: int) -> int | None:
+    """_ptr for a tensor that has to be on device `dev`; the calls of a small
+    batch are bound by the time spent here, so the good case is one line."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.numel() == numel \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _ptr(t, name, dtype, numel)
+    raise ValueError(f"{name}: expected a tensor on cuda:{dev}, got {t.device}")
+
+
+def _call(name: str, dev: int, stream, *args) -> None:
+    """The C call with the tensors' device current, so that the launch and the
+    default stream are that device's."""
+    if dev < 0:
+        raise ValueError(f"{name}: expected CUDA tensors (the library computes on the GPU only)")
+    fn = getattr(lib, name)
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
+        raise ValueError(f"{name}: tensors on cuda:{dev}, stream on {stream.device}")
+    if dev == torch.cuda.current_device():
+        s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream(stream))
+    if status != 0:
+        raise DSparkError(name, status)
 
 
 def dspark_logprobs(logits, tokens, logprob, entropy, stats, top_tokens, top_logprobs, workspace, row_start=None,
@@ -335,23 +351,26 @@ def dspark_logprobs(logits, tokens, logprob, entropy, stats, top_tokens, top_log
     None; top_k is their last dimension."""
     dt = _dtype(logits, "logits")
     ptr, n_rows, V, ld = _rows(logits, "logits")
+    dev = logits.get_device()
     B, C = tokens.shape
-    n = B * C
+    n, k = B * C, 0
     if (top_tokens is None) != (top_logprobs is None):
         raise ValueError("top_tokens and top_logprobs: give both or neither")
-    k = 0
     if top_tokens is not None:
         if top_tokens.dim() != 3:
             raise ValueError("top_tokens: expected [B,C,top_k]")
-        k = top_tokens.shape[-1]
-    args = (ptr, dt, n_rows, ld, _ptr(row_start, "row_start", torch.int64, B), _ptr(tokens, "tokens", torch.int32),
-            B, C, V, k, _ptr(logprob, "logprob", torch.float32, n), _ptr(entropy, "entropy", torch.float32, n),
-            _ptr(stats, "stats", torch.float32, 2 * n), _ptr(top_tokens, "top_tokens", torch.int32, n * k),
-            _ptr(top_logprobs, "top_logprobs", torch.float32, n * k), _ptr(workspace, "workspace", torch.uint8),
-            workspace.numel())
-    _on_device("dspark_logprobs", logits,
-               (tokens, logprob, entropy, stats, top_tokens, top_logprobs, workspace, row_start), stream,
-               lambda s: lib.dspark_logprobs(*args, s))
+        k = top_tokens.shape[2]
+    f32, i32 = torch.float32, torch.int32
+    _call("dspark_logprobs", dev, stream, ptr, dt, n_rows, ld, _on(dev, row_start, "row_start", torch.int64, B),
+          _on(dev, tokens, "tokens", i32, n), B, C, V, k, _on(dev, logprob, "logprob", f32, n),
+          _on(dev, entropy, "entropy", f32, n), _on(dev, stats, "stats", f32, 2 * n),
+          _on(dev, top_tokens, "top_tokens", i32, n * k), _on(dev, top_logprobs, "top_logprobs", f32, n * k),
+          *_workspace(dev, workspace))
+
+
+def _workspace(dev: int, workspace: torch.Tensor) -> tuple[int, int]:
+    size = workspace.numel()
+    return _on(dev, workspace, "workspace", torch.uint8, size), size
 
 
 def dspark_logprobs_grad(logits, tokens, stats, entropy, g_logprob, g_entropy, dlogits, workspace,
@@ -364,28 +383,27 @@ def dspark_logprobs_grad(logits, tokens, stats, entropy, g_logprob, g_entropy, d
         raise TypeError("dlogits: expected the type of logits")
     ptr, N, V, ld = _rows(logits, "logits")
     gptr, gN, gV, gld = _rows(dlogits, "dlogits")
-    if (gN, gV) != (N, V):
+    if gN != N or gV != V:
         raise ValueError(f"dlogits: expected [{N},{V}], got [{gN},{gV}]")
     if g_entropy is not None and entropy is None:
         raise ValueError("entropy: needed with g_entropy")
-    args = (ptr, dt, ld, _ptr(tokens, "tokens", torch.int32, N), _ptr(stats, "stats", torch.float32, 2 * N),
-            _ptr(entropy, "entropy", torch.float32, N), _ptr(g_logprob, "g_logprob", torch.float32, N),
-            _ptr(g_entropy, "g_entropy", torch.float32, N), N, V, gptr, gld,
-            _ptr(workspace, "workspace", torch.uint8), workspace.numel())
-    _on_device("dspark_logprobs_grad", logits,
-               (tokens, stats, entropy, g_logprob, g_entropy, dlogits, workspace), stream,
-               lambda s: lib.dspark_logprobs_grad(*args, s))
+    dev, f32 = logits.get_device(), torch.float32
+    if dlogits.get_device() != dev:
+        raise ValueError(f"dlogits: expected a tensor on cuda:{dev}, got {dlogits.device}")
+    _call("dspark_logprobs_grad", dev, stream, ptr, dt, ld, _on(dev, tokens, "tokens", torch.int32, N),
+          _on(dev, stats, "stats", f32, 2 * N), _on(dev, entropy, "entropy", f32, N),
+          _on(dev, g_logprob, "g_logprob", f32, N), _on(dev, g_entropy, "g_entropy", f32, N), N, V, gptr, gld,
+          *_workspace(dev, workspace))
 
 
 def dspark_embed(table, tokens, scale: float, out, workspace, stream=None) -> None:
     """out [n,r] = scale * table[tokens] (zeros for a token of -1); table [V,r]
     and out each float32 or bfloat16."""
     V, r = table.shape
-    n = tokens.numel()
-    args = (_ptr(table, "table"), _dtype(table, "table"), _ptr(tokens, "tokens", torch.int32), n, V, r, float(scale),
-            _ptr(out, "out", numel=n * r), _dtype(out, "out"), _ptr(workspace, "workspace", torch.uint8),
-            workspace.numel())
-    _on_device("dspark_embed", table, (tokens, out, workspace), stream, lambda s: lib.dspark_embed(*args, s))
+    n, dev = tokens.numel(), table.get_device()
+    _call("dspark_embed", dev, stream, _on(dev, table, "table", table.dtype, V * r), _dtype(table, "table"),
+          _on(dev, tokens, "tokens", torch.int32, n), n, V, r, scale, _on(dev, out, "out", out.dtype, n * r),
+          _dtype(out, "out"), *_workspace(dev, workspace))
 
 
 def dspark_embed_grad_workspace_bytes(n: int, V: int, r: int) -> int:
@@ -399,12 +417,10 @@ def dspark_embed_grad(dout, tokens, scale: float, dtable, workspace, accumulate:
     """dtable [V,r] = (accumulate: +=) scale * the sum of dout's rows [n,r] over
     the items of each token; dout and dtable each float32 or bfloat16."""
     V, r = dtable.shape
-    n = tokens.numel()
-    args = (_ptr(dout, "dout", numel=n * r), _dtype(dout, "dout"), _ptr(tokens, "tokens", torch.int32), n, V, r,
-            float(scale), int(bool(accumulate)), _ptr(dtable, "dtable"), _dtype(dtable, "dtable"),
-            _ptr(workspace, "workspace", torch.uint8), workspace.numel())
-    _on_device("dspark_embed_grad", dtable, (dout, tokens, workspace), stream,
-               lambda s: lib.dspark_embed_grad(*args, s))
+    n, dev = tokens.numel(), dtable.get_device()
+    _call("dspark_embed_grad", dev, stream, _on(dev, dout, "dout", dout.dtype, n * r), _dtype(dout, "dout"),
+          _on(dev, tokens, "tokens", torch.int32, n), n, V, r, scale, 1 if accumulate else 0,
+          _on(dev, dtable, "dtable", dtable.dtype, V * r), _dtype(dtable, "dtable"), *_workspace(dev, workspace))
 
 
 DSPARK_INJECT_NONE, DSPARK_INJECT_DRAFT_SLICE_SUMS, DSPARK_INJECT_VERIFY_BARRIER = 0, 1, 2

@@ -10,6 +10,8 @@ namespace {
 constexpr int kMaxItems = 1 << 24;
 constexpr int kMaxSms = 148;   // owners of table rows, one CTA each (more only for very large V)
 
+__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(uint16_t x) { return bf16_bits_to_float(x); }
 
@@ -39,15 +41,107 @@ struct EmbedArgs {
 
 constexpr int kThreads = 256;
 
-template <typename TI, typename TO>
+// Eight neighbouring columns as they are held.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<float> {
+  float4 lo, hi;
+  __device__ __forceinline__ void load(const float* p) {
+    lo = __ldg(reinterpret_cast<const float4*>(p));
+    hi = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
+    v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+  }
+  __device__ __forceinline__ static void save(float* p, const float (&v)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+};
+template <>
+struct Eight<uint16_t> {
+  uint4 u;
+  __device__ __forceinline__ void load(const uint16_t* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const unsigned w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ static void save(uint16_t* p, const float (&v)[8]) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  }
+};
+
+// blockDim.x threads a row (eight columns each, or single ones where r is no
+// multiple of 8), blockDim.y * kRows rows a CTA, kRows of them in flight a
+// thread.
+template <typename TI, typename TO, bool kVec, int kRows>
 __global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a) {
-  const int i = blockIdx.x;
-  const int t = a.tokens[i];
-  TO* out = static_cast<TO*>(a.out) + static_cast<long long>(i) * a.r;
-  const bool ok = t >= 0 && t < a.V;
-  if (!ok && t != -1 && threadIdx.x == 0) record_bad_token(a.err, i);
-  const TI* row = static_cast<const TI*>(a.table) + static_cast<long long>(ok ? t : 0) * a.r;
-  for (int k = threadIdx.x; k < a.r; k += kThreads) store(out + k, ok ? to_float(row[k]) * a.scale : 0.f);
+  const int i0 = blockIdx.x * blockDim.y * kRows + threadIdx.y;
+  int t[kRows];
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const int i = i0 + u * blockDim.y;
+    t[u] = i < a.n ? __ldg(a.tokens + i) : -1;
+    if (t[u] < -1 || t[u] >= a.V) {
+      if (threadIdx.x == 0) record_bad_token(a.err, i);
+      t[u] = -1;
+    }
+  }
+  const TI* table = static_cast<const TI*>(a.table);
+  TO* out = static_cast<TO*>(a.out);
+  if constexpr (kVec) {
+    for (int c = threadIdx.x * 8; c < a.r; c += blockDim.x * 8) {
+      Eight<TI> x[kRows];
+#pragma unroll
+      for (int u = 0; u < kRows; ++u)
+        if (t[u] >= 0) x[u].load(table + static_cast<long long>(t[u]) * a.r + c);
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        const int i = i0 + u * blockDim.y;
+        if (i >= a.n) continue;
+        float v[8];
+        x[u].get(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = t[u] >= 0 ? v[j] * a.scale : 0.f;
+        Eight<TO>::save(out + static_cast<long long>(i) * a.r + c, v);
+      }
+    }
+  } else {
+    for (int c = threadIdx.x; c < a.r; c += blockDim.x) {
+      float v[kRows];
+#pragma unroll
+      for (int u = 0; u < kRows; ++u)
+        v[u] = t[u] >= 0 ? to_float(__ldg(table + static_cast<long long>(t[u]) * a.r + c)) * a.scale : 0.f;
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        const int i = i0 + u * blockDim.y;
+        if (i < a.n) store(out + static_cast<long long>(i) * a.r + c, v[u]);
+      }
+    }
+  }
+}
+
+template <typename TI, typename TO>
+cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t s) {
+  const bool vec = a.r % 8 == 0;
+  const int units = vec ? a.r / 8 : a.r;
+  int x = 8;
+  while (x < units && x < kThreads) x *= 2;
+  const dim3 block(x, kThreads / x);
+  // four rows a thread once that fills the GPU
+  const int rows = static_cast<long long>(a.n) >= 8ll * kMaxSms * block.y ? 4 : 1;
+  const int grid = ceil_div(a.n, static_cast<int>(block.y) * rows);
+  auto kernel = vec ? (rows == 4 ? embed_kernel<TI, TO, true, 4> : embed_kernel<TI, TO, true, 1>)
+                    : (rows == 4 ? embed_kernel<TI, TO, false, 4> : embed_kernel<TI, TO, false, 1>);
+  kernel<<<grid, block, 0, s>>>(a);
+  return cudaGetLastError();
 }
 
 // -------------------------------------------------------------- gradient
@@ -90,8 +184,6 @@ constexpr int kSumWarps = 8, kSumThreads = kSumWarps * 32;
 constexpr int kSlab = 128;      // columns of a warp: four a lane
 constexpr int kDirectItems = 1024;
 constexpr int kDirectThreads = 128;
-
-__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 template <typename TO>
 __device__ __forceinline__ void zero_row(TO* d, int r, int lane) {
@@ -527,11 +619,11 @@ dspark_status dspark_embed(const void* table, dspark_dtype table_dtype, const in
   const EmbedArgs a{table, tokens, n, V, r, scale, out,
                     reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + kErrOffset)};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  auto kernel = table_dtype == DSPARK_F32
-                    ? (out_dtype == DSPARK_F32 ? embed_kernel<float, float> : embed_kernel<float, uint16_t>)
-                    : (out_dtype == DSPARK_F32 ? embed_kernel<uint16_t, float> : embed_kernel<uint16_t, uint16_t>);
-  kernel<<<n, kThreads, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  const cudaError_t e = table_dtype == DSPARK_F32
+                            ? (out_dtype == DSPARK_F32 ? launch_embed<float, float>(a, s) : launch_embed<float, uint16_t>(a, s))
+                            : (out_dtype == DSPARK_F32 ? launch_embed<uint16_t, float>(a, s)
+                                                       : launch_embed<uint16_t, uint16_t>(a, s));
+  return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 size_t dspark_embed_grad_workspace_bytes(int n, int V, int r) {

@@ -5,7 +5,9 @@
 //   S = sum 2^y,  T = sum y 2^y,  y = (x - m) log2 e,
 // so that ln p_v = x_v - m - ln S and the entropy is ln S - ln 2 T/S. The
 // difference x - m is taken before the product, so that masks of the type's
-// lowest value, and rows with nothing else, stay within range.
+// lowest value, and rows with nothing else, stay within range. Each lane
+// carries its own m, S and T through one pass over the row (a larger m scales
+// S and T) and the lanes' triples are joined at the end.
 #include <algorithm>
 
 #include "common.cuh"
@@ -17,6 +19,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr double kLn2 = 0.69314718055994530942;
 constexpr int kMaxItems = 1 << 24;
 constexpr long long kMaxStride = 1ll << 32;
+constexpr int kSms = 148;
 // exponents below this give 2^y = 0; the clamp keeps y 2^y from being -inf * 0
 constexpr float kMinExp = -16384.f;
 
@@ -32,6 +35,9 @@ struct ScoreArgs {
   int32_t* top_tokens;
   float* top_logprobs;
   unsigned* err;
+  int parts;   // CTAs of a cluster, each with an equal part of the row
+  int group;   // tiles of a segment (alternatives)
+  int room;    // candidates that shared memory holds
 };
 
 struct GradArgs {
@@ -45,146 +51,591 @@ struct GradArgs {
   int V;
   void* dlogits;
   unsigned* err;
+  int pieces;  // CTAs of a row
 };
 
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(uint16_t x) { return bf16_bits_to_float(x); }
 
+// Two fp32 values as a pair of bf16, rounded to nearest even.
+__device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
+  unsigned r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ void store(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store(uint16_t* p, float v) {
-  asm volatile("{ .reg .b16 h; cvt.rn.bf16.f32 h, %1; st.global.b16 [%0], h; }" ::"l"(p), "f"(v) : "memory");
+__device__ __forceinline__ void store(uint16_t* p, float v) { *p = static_cast<uint16_t>(pack_bf16(v, 0.f)); }
+
+// 2^y, relative error below 2^-22; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float y) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+  return r;
 }
 
-// Order of the alternatives as one number: the logit's order (NaN as -inf, -0
-// as 0), then the lowest token.
-__device__ __forceinline__ unsigned long long rank_key(float x, int v) {
-  x = fmaxf(x, -INFINITY) + 0.f;
-  const unsigned b = __float_as_uint(x);
-  const unsigned o = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-  return (static_cast<unsigned long long>(o) << 32) | (0xffffffffu - static_cast<unsigned>(v));
+// The j-th pair of a 16-byte vector's elements, and the vector's length.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int kLen = 4;
+  static constexpr unsigned kNegInf = 0xff800000u;
+  __device__ __forceinline__ static F2 pair(const uint4& v, int j) {
+    return j == 0 ? f2(__uint_as_float(v.x), __uint_as_float(v.y)) : f2(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+  __device__ __forceinline__ static uint4 pack(const F2 (&d)[2]) {
+    return make_uint4(__float_as_uint(f2_lo(d[0])), __float_as_uint(f2_hi(d[0])), __float_as_uint(f2_lo(d[1])),
+                      __float_as_uint(f2_hi(d[1])));
+  }
+  __device__ __forceinline__ static float largest(const uint4& v) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
+};
+template <>
+struct Vec<uint16_t> {
+  static constexpr int kLen = 8;
+  static constexpr unsigned kNegInf = 0xff80ff80u;
+  __device__ __forceinline__ static F2 pair(const uint4& v, int j) {
+    const unsigned u = j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+    return f2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+  __device__ __forceinline__ static uint4 pack(const F2 (&d)[4]) {
+    return make_uint4(pack_bf16(f2_lo(d[0]), f2_hi(d[0])), pack_bf16(f2_lo(d[1]), f2_hi(d[1])),
+                      pack_bf16(f2_lo(d[2]), f2_hi(d[2])), pack_bf16(f2_lo(d[3]), f2_hi(d[3])));
+  }
+  __device__ __forceinline__ static unsigned max2(unsigned a, unsigned b) {   // NaN gives way
+    unsigned d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  __device__ __forceinline__ static float largest(const uint4& v) {
+    const unsigned m = max2(max2(v.x, v.y), max2(v.z, v.w));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+};
+
+// A row as 16-byte vectors: `head` elements in front of the first aligned one,
+// nvec vectors, `tail` elements behind.
+template <typename T>
+struct Row {
+  const T* x;
+  int head, nvec, tail;
+  __device__ __forceinline__ Row(const T* p, int V) : x(p) {
+    constexpr int E = Vec<T>::kLen;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
+    head = min(V, (E - off) % E);
+    nvec = (V - head) / E;
+    tail = V - head - nvec * E;
+  }
+  __device__ __forceinline__ const uint4* vecs() const { return reinterpret_cast<const uint4*>(x + head); }
+};
+
+// --------------------------------------------------------------- scores
+
+constexpr int kAhead = 8;                 // vectors of a lane in flight
+constexpr int kTile = 32 * kAhead;        // vectors of a tile: one warp, one step
+constexpr int kMaxWarps = 16;
+constexpr int kMaxSegs = 256;             // segments of a CTA's part
+constexpr int kRoom = 2048;               // candidates beside the top_k that are kept
+
+// Largest logit, sum and tilted sum of some elements of a row.
+struct Triple {
+  float m;
+  double S, T;
+};
+
+__device__ __forceinline__ Triple join(const Triple& a, const Triple& b) {
+  Triple r;
+  r.m = fmaxf(a.m, b.m);
+  if (r.m == -INFINITY) {       // no finite element: S and T are 0 or NaN
+    r.S = a.S + b.S;
+    r.T = a.T + b.T;
+    return r;
+  }
+  // an empty side (m = -inf) has S = T = 0, or NaN
+  const float da = a.m == -INFINITY ? 0.f : (r.m - a.m) * kLog2e, db = b.m == -INFINITY ? 0.f : (r.m - b.m) * kLog2e;
+  const double fa = ex2(-da), fb = ex2(-db);
+  r.S = a.S * fa + b.S * fb;
+  r.T = (fa > 0.0 ? (a.T - da * a.S) * fa : a.S * 0.0) + (fb > 0.0 ? (b.T - db * b.S) * fb : b.S * 0.0);
+  return r;
 }
-__device__ __forceinline__ float key_value(unsigned long long k) {
-  const unsigned o = static_cast<unsigned>(k >> 32);
+
+// Adds the kCount vectors v to the lane's triple, whose m is at least as large
+// as every element; sums of at most 64 terms are fp32.
+template <typename T, int kCount>
+__device__ __forceinline__ void add_terms(const uint4 (&v)[kCount], float m, double& S, double& Tsum) {
+  const float shift = m == -INFINITY ? 0.f : m;
+  const F2 ns = f2(-shift, -shift), l2e = f2(kLog2e, kLog2e);
+  F2 s = f2(0.f, 0.f), t = f2(0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < kCount; ++k) {
+#pragma unroll
+    for (int j = 0; j < Vec<T>::kLen / 2; ++j) {
+      const F2 y0 = mul2(add2(Vec<T>::pair(v[k], j), ns), l2e);
+      const F2 y = f2(fmax_nan(f2_lo(y0), kMinExp), fmax_nan(f2_hi(y0), kMinExp));
+      const F2 e = f2(ex2(f2_lo(y)), ex2(f2_hi(y)));
+      s = add2(s, e);
+      t = fma2(e, y, t);
+    }
+  }
+  S += static_cast<double>(f2_lo(s)) + static_cast<double>(f2_hi(s));
+  Tsum += static_cast<double>(f2_lo(t)) + static_cast<double>(f2_hi(t));
+}
+
+// Moves a triple to a larger m.
+__device__ __forceinline__ void raise(float& m, double& S, double& Tsum, float to) {
+  if (!(to > m)) return;
+  if (m != -INFINITY) {
+    const float d = (to - m) * kLog2e;
+    const double f = ex2(-d);
+    Tsum = f > 0.0 ? (Tsum - d * S) * f : S * 0.0;
+    S *= f;
+  }
+  m = to;
+}
+
+// The alternatives' order as one number: the logit's order (-0 as 0), then the
+// lowest token. No alternative is 0. NaN and -inf are no candidates.
+__device__ __forceinline__ unsigned order_of(float x) {
+  const unsigned b = __float_as_uint(x + 0.f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ unsigned long long rank_key(float x, int v) {
+  return (static_cast<unsigned long long>(order_of(x)) << 32) | (0xffffffffu - static_cast<unsigned>(v));
+}
+__device__ __forceinline__ float order_value(unsigned o) {
   return __uint_as_float((o & 0x80000000u) ? (o ^ 0x80000000u) : ~o);
 }
 __device__ __forceinline__ int key_token(unsigned long long k) {
   return static_cast<int>(0xffffffffu - static_cast<unsigned>(k));
 }
 
-constexpr int kThreads = 256;
+// The k largest of n different keys, in order, to `out` (0 behind the n-th).
+// Few keys: each thread counts the keys above its own. Many: the k-th largest
+// is found bit by bit first, which leaves k. All threads of the CTA call.
+__device__ void take_largest(unsigned long long* keys, int n, int k, unsigned long long* out, int* s_count) {
+  const int tid = threadIdx.x, nt = blockDim.x;
+  if (n > 512) {
+    unsigned long long kth = 0ull;
+    for (int bit = 63; bit >= 0; --bit) {
+      const unsigned long long c = kth | (1ull << bit);
+      int mine = 0;
+      for (int i = tid; i < n; i += nt) mine += keys[i] >= c;
+      if (tid == 0) *s_count = 0;
+      __syncthreads();
+      mine = __reduce_add_sync(0xffffffffu, mine);
+      if ((tid & 31) == 0 && mine != 0) atomicAdd(s_count, mine);
+      __syncthreads();
+      const int above = *s_count;
+      __syncthreads();
+      if (above >= k) kth = c;
+    }
+    // n > 512 >= k keys, all different: exactly k are >= kth. They go to `out`
+    // in any order, then in order to the front of the list.
+    if (tid == 0) *s_count = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += nt)
+      if (keys[i] >= kth) out[atomicAdd(s_count, 1)] = keys[i];
+    __syncthreads();
+    for (int i = tid; i < k; i += nt) keys[i] = out[i];
+    n = k;
+    __syncthreads();
+  }
+  for (int i = tid; i < k; i += nt)
+    if (i >= n) out[i] = 0ull;
+  for (int i = tid; i < n; i += nt) {
+    const unsigned long long key = keys[i];
+    int above = 0;
+    for (int j = 0; j < n; ++j) above += keys[j] > key;
+    if (above < k) out[above] = key;
+  }
+  __syncthreads();
+}
 
-// One CTA a row, one pass for the sums and one for each alternative.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(ScoreArgs a) {
-  __shared__ double redd[33];
-  __shared__ float redf[33];
-  __shared__ unsigned long long s_best;
-  const int item = blockIdx.x, tid = threadIdx.x, V = a.V;
-  const int b = item / a.C, c = item - b * a.C;
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The other CTA's copy of a shared 64-bit word.
+__device__ __forceinline__ unsigned long long read_peer(const void* p, int rank) {
+  unsigned a;
+  unsigned long long v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(a)
+               : "r"(static_cast<unsigned>(__cvta_generic_to_shared(p))), "r"(rank));
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// One cluster of `parts` CTAs an item, each with an equal part of the row's
+// tiles. Alternatives: the top_k elements lie in the top_k segments with the
+// largest maxima (equal ones: the first), because each segment in front of
+// another holds an element in front of all of the other's. The pass over the
+// row notes the segments' maxima only; the chosen segments are read again for
+// the elements that reach the last one's maximum.
+template <typename T, bool kTop>
+__global__ void __launch_bounds__(kMaxWarps * 32, 2) logprobs_kernel(ScoreArgs a) {
+  constexpr int E = Vec<T>::kLen;
+  extern __shared__ unsigned long long s_keys[];        // [room]
+  __shared__ unsigned s_seg[kTop ? kMaxSegs : 1];
+  __shared__ int s_chosen[32];
+  __shared__ unsigned long long s_top[32];
+  __shared__ int s_count;
+  __shared__ unsigned s_tau;
+  __shared__ double s_S[kMaxWarps], s_T[kMaxWarps];
+  __shared__ float s_m[kMaxWarps];
+  __shared__ unsigned long long s_mine[3];              // the CTA's triple, for the cluster
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, nt = blockDim.x, W = nt >> 5;
+  const int parts = a.parts, part = parts > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int item = blockIdx.x / parts, V = a.V, k = a.top_k;
+  const int b = item / a.C;
   const int tok = a.tokens[item];
   bool skip = tok == -1;
-  const long long row = a.row_start != nullptr ? a.row_start[b] + c : static_cast<long long>(item);
+  const long long row = a.row_start != nullptr ? a.row_start[b] + (item - b * a.C) : static_cast<long long>(item);
   if (!skip && (tok < 0 || tok >= V || row < 0 || row >= a.n_rows)) {
-    if (tid == 0) set_error(a.err, DSPARK_ERR_DEVICE_ASSERT, 0x70000000u | static_cast<unsigned>(item));
+    if (tid == 0 && part == 0) set_error(a.err, DSPARK_ERR_DEVICE_ASSERT, 0x70000000u | static_cast<unsigned>(item));
     skip = true;
   }
-  if (skip) {
+  if (skip) {                       // the same for every CTA of the cluster
+    if (part != 0) return;
     if (tid == 0) {
       a.logprob[item] = 0.f;
       if (a.entropy != nullptr) a.entropy[item] = 0.f;
-      if (a.stats != nullptr) a.stats[2ll * item] = a.stats[2ll * item + 1] = 0.f;
+      if (a.stats != nullptr) reinterpret_cast<float2*>(a.stats)[item] = make_float2(0.f, 0.f);
     }
-    for (int i = tid; i < a.top_k; i += kThreads) {
-      a.top_tokens[static_cast<long long>(item) * a.top_k + i] = -1;
-      a.top_logprobs[static_cast<long long>(item) * a.top_k + i] = -INFINITY;
+    for (int i = tid; kTop && i < k; i += nt) {
+      a.top_tokens[static_cast<long long>(item) * k + i] = -1;
+      a.top_logprobs[static_cast<long long>(item) * k + i] = -INFINITY;
     }
     return;
   }
-  const T* x = static_cast<const T*>(a.logits) + row * a.stride;
+  const Row<T> r(static_cast<const T*>(a.logits) + row * a.stride, V);
+  const uint4* vecs = r.vecs();
+  const float xt = part == 0 && tid == 0 ? to_float(r.x[tok]) : 0.f;
+  const int tiles = (r.nvec + kTile - 1) / kTile;
+  const int t0 = static_cast<int>(static_cast<long long>(tiles) * part / parts);
+  const int t1 = static_cast<int>(static_cast<long long>(tiles) * (part + 1) / parts);
+  const int segs = (t1 - t0 + a.group - 1) / a.group;
+  if (kTop && a.group > 1) {
+    for (int i = tid; i < segs; i += nt) s_seg[i] = 0u;
+    __syncthreads();
+  }
+
   float m = -INFINITY;
-  for (int v = tid; v < V; v += kThreads) m = fmaxf(m, to_float(x[v]));
-  m = block_max<kThreads>(m, redf);
-  const float shift = m == -INFINITY ? 0.f : m;
   double S = 0.0, Tsum = 0.0;
-  for (int v = tid; v < V; v += kThreads) {
-    const float y = fmax_nan((to_float(x[v]) - shift) * kLog2e, kMinExp);
-    const float e = exp2f(y);
+  for (int t = t0 + w; t < t1; t += W) {
+    uint4 v[kAhead];
+    const int i0 = t * kTile + lane;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const unsigned ni = Vec<T>::kNegInf;
+      v[u] = i0 + u * 32 < r.nvec ? __ldg(vecs + i0 + u * 32) : make_uint4(ni, ni, ni, ni);
+    }
+    float most = Vec<T>::largest(v[0]);
+#pragma unroll
+    for (int u = 1; u < kAhead; ++u) most = fmaxf(most, Vec<T>::largest(v[u]));
+    raise(m, S, Tsum, most);
+    add_terms<T>(v, m, S, Tsum);
+    if (kTop) {
+      const unsigned o = __reduce_max_sync(0xffffffffu, order_of(fmaxf(most, -INFINITY)));
+      if (lane == 0) {
+        if (a.group == 1)
+          s_seg[t - t0] = o;
+        else
+          atomicMax(&s_seg[(t - t0) / a.group], o);
+      }
+    }
+  }
+  // the ends outside the vectors: at most kLen - 1 elements each
+  const int ends = (part == 0 ? r.head : 0) + (part == parts - 1 ? r.tail : 0);
+  int end_at = -1;
+  float end_x = -INFINITY;
+  if (w == 0 && lane < ends) {
+    end_at = part == 0 && lane < r.head ? lane : V - ends + lane;
+    end_x = to_float(r.x[end_at]);
+    raise(m, S, Tsum, end_x);
+    const float y = fmax_nan((end_x - (m == -INFINITY ? 0.f : m)) * kLog2e, kMinExp), e = ex2(y);
     S += e;
     Tsum += static_cast<double>(e * y);
   }
-  S = block_sum<kThreads>(S, redd);
-  Tsum = block_sum<kThreads>(Tsum, redd);
-  const double lnS = log(S);
-  const bool bad = !(S < 1e300);  // a NaN or +inf in the row
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Triple other{__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, S, o),
+                       __shfl_xor_sync(0xffffffffu, Tsum, o)};
+    const Triple own{m, S, Tsum};
+    const Triple j = (lane & o) ? join(other, own) : join(own, other);
+    m = j.m;
+    S = j.S;
+    Tsum = j.T;
+  }
+  if (lane == 0) {
+    s_m[w] = m;
+    s_S[w] = S;
+    s_T[w] = Tsum;
+  }
+  if (tid == 0) s_count = 0;
+  __syncthreads();
+  Triple all{s_m[0], s_S[0], s_T[0]};
   if (tid == 0) {
-    const float xt = to_float(x[tok]);
+    for (int j = 1; j < W; ++j) all = join(all, Triple{s_m[j], s_S[j], s_T[j]});
+    s_mine[0] = __float_as_uint(all.m);
+    s_mine[1] = __double_as_longlong(all.S);
+    s_mine[2] = __double_as_longlong(all.T);
+  }
+
+  if (kTop) {
+    // the segments to read again
+    const int chosen = min(k, segs);
+    for (int i = tid; i < segs; i += nt) {
+      const unsigned o = s_seg[i];
+      int above = 0;
+      for (int j = 0; j < segs; ++j) above += s_seg[j] > o || (s_seg[j] == o && j < i);
+      if (above < k) s_chosen[above] = i;
+      if (above == k - 1) s_tau = o;
+    }
+    __syncthreads();
+    // below tau there is nothing to find; -inf is never a candidate
+    const float tau = segs >= k ? order_value(s_tau) : -INFINITY;
+    const int units = chosen * a.group * kAhead;       // rows of 32 vectors
+    auto vec_of = [&](int unit) {                      // the lane's vector, -1: none
+      const int tile = t0 + s_chosen[unit / (a.group * kAhead)] * a.group + unit / kAhead % a.group;
+      const int i = tile * kTile + unit % kAhead * 32 + lane;
+      return tile < t1 && i < r.nvec ? i : -1;
+    };
+    auto offer = [&](float x, int v, unsigned long long above, int room) {
+      if (!(x >= tau) || x == -INFINITY) return;
+      const unsigned long long key = rank_key(x, v);
+      if (key <= above) return;
+      const int at = atomicAdd(&s_count, 1);
+      if (at < room) s_keys[at] = key;
+    };
+    auto offer_vec = [&](int i, const uint4& v, unsigned long long above, int room) {
+      if (i < 0 || !(Vec<T>::largest(v) >= tau)) return;
+#pragma unroll
+      for (int j = 0; j < E / 2; ++j) {
+        const F2 p = Vec<T>::pair(v, j);
+        offer(f2_lo(p), r.head + i * E + 2 * j, above, room);
+        offer(f2_hi(p), r.head + i * E + 2 * j + 1, above, room);
+      }
+    };
+    if (end_at >= 0) offer(end_x, end_at, 0ull, a.room);
+    for (int u0 = w; u0 < units; u0 += 4 * W) {
+      int i[4];
+      uint4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        i[q] = u0 + q * W < units ? vec_of(u0 + q * W) : -1;
+        if (i[q] >= 0) v[q] = __ldg(vecs + i[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) offer_vec(i[q], v[q], 0ull, a.room);
+    }
+    __syncthreads();
+    const int found = s_count;
+    __syncthreads();
+    if (found <= a.room) {
+      take_largest(s_keys, found, k, s_top, &s_count);
+    } else {
+      // more candidates than room (many equal or sorted logits): as many units
+      // at a time as fit beside the best so far, which raise the bar
+      const int step = (a.room - 32) / (32 * E);       // room is at least 32 + 32 E
+      int have = 0;
+      unsigned long long bar = 0ull;
+      for (int u0 = 0; u0 < units; u0 += step) {
+        if (tid == 0) s_count = have;
+        __syncthreads();
+        if (u0 == 0 && end_at >= 0) offer(end_x, end_at, 0ull, a.room);
+        for (int u = u0 + w; u < min(units, u0 + step); u += W) {
+          const int i = vec_of(u);
+          if (i >= 0) offer_vec(i, __ldg(vecs + i), bar, a.room);
+        }
+        __syncthreads();
+        const int n = s_count;
+        __syncthreads();
+        take_largest(s_keys, n, k, s_top, &s_count);
+        have = min(n, k);
+        for (int i = tid; i < have; i += nt) s_keys[i] = s_top[i];
+        if (n >= k) bar = s_top[k - 1];
+        __syncthreads();
+      }
+    }
+  }
+
+  if (parts > 1) {
+    cluster_sync();
+    if (part == 0) {
+      if (tid == 0)
+        for (int p = 1; p < parts; ++p)
+          all = join(all, Triple{__uint_as_float(static_cast<unsigned>(read_peer(&s_mine[0], p))),
+                                 __longlong_as_double(read_peer(&s_mine[1], p)),
+                                 __longlong_as_double(read_peer(&s_mine[2], p))});
+      if (kTop) {
+        if (tid == 0) s_count = 0;
+        __syncthreads();
+        for (int i = tid; i < parts * k; i += nt) {
+          const unsigned long long key = i < k ? s_top[i] : read_peer(&s_top[i % k], i / k);
+          if (key != 0ull) s_keys[atomicAdd(&s_count, 1)] = key;    // room >= 8 * 32
+        }
+        __syncthreads();
+        const int n = s_count;
+        __syncthreads();
+        take_largest(s_keys, n, k, s_top, &s_count);
+      }
+    }
+    cluster_sync();
+    if (part != 0) return;
+  }
+  const bool bad = !(all.S < 1e300);   // a NaN or +inf in the row
+  if (tid == 0) {
+    const double shift = all.m == -INFINITY ? 0.0 : static_cast<double>(all.m), lnS = log(all.S);
     float lp = xt == -INFINITY ? xt : static_cast<float>(static_cast<double>(xt) - shift - lnS);
-    float H = S > 0.0 ? static_cast<float>(lnS - kLn2 * (Tsum / S)) : 0.f;
+    float H = all.S > 0.0 ? static_cast<float>(lnS - kLn2 * (all.T / all.S)) : 0.f;
     if (bad) lp = H = NAN;
     a.logprob[item] = lp;
     if (a.entropy != nullptr) a.entropy[item] = H;
-    if (a.stats != nullptr) {
-      a.stats[2ll * item] = bad ? NAN : m;
-      a.stats[2ll * item + 1] = bad ? NAN : static_cast<float>(S);
+    if (a.stats != nullptr)
+      reinterpret_cast<float2*>(a.stats)[item] = bad ? make_float2(NAN, NAN) : make_float2(all.m, static_cast<float>(all.S));
+    if (kTop) {
+      s_S[0] = shift;
+      s_T[0] = lnS;
+      s_count = bad;
     }
   }
-  unsigned long long last = ~0ull;
-  for (int i = 0; i < a.top_k; ++i) {
-    if (tid == 0) s_best = 0ull;
+  if (kTop) {
     __syncthreads();
-    unsigned long long best = 0ull;
-    for (int v = tid; v < V; v += kThreads) {
-      const unsigned long long k = rank_key(to_float(x[v]), v);
-      if (k < last && k > best) best = k;
-    }
-    atomicMax(&s_best, best);
-    __syncthreads();
-    last = s_best;
-    __syncthreads();
-    if (tid == 0) {
-      const long long o = static_cast<long long>(item) * a.top_k + i;
-      const float xv = last == 0ull ? -INFINITY : key_value(last);
-      a.top_tokens[o] = xv == -INFINITY ? -1 : key_token(last);
-      a.top_logprobs[o] = bad ? NAN
-                          : xv == -INFINITY
-                              ? xv
-                              : static_cast<float>(static_cast<double>(xv) - shift - lnS);
+    const double shift = s_S[0], lnS = s_T[0];
+    for (int i = tid; i < k; i += nt) {
+      const unsigned long long key = s_top[i];
+      const long long o = static_cast<long long>(item) * k + i;
+      const float none = s_count ? NAN : -INFINITY;
+      a.top_tokens[o] = key != 0ull ? key_token(key) : -1;
+      a.top_logprobs[o] = key == 0ull || s_count
+                              ? none
+                              : static_cast<float>(order_value(static_cast<unsigned>(key >> 32)) - shift - lnS);
     }
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(GradArgs a) {
-  const int row = blockIdx.x, tid = threadIdx.x, V = a.V;
-  const T* x = static_cast<const T*>(a.logits) + row * a.stride;
+// ------------------------------------------------------------- gradient
+
+constexpr int kGradThreads = 256;
+constexpr int kGradAhead = 4;
+
+// dlogits_v = p_v (c0 + c1 y_v) + g [v = t]: with y = (x - m) log2 e,
+// p = 2^y / s and ln p = y ln 2 - ln s, the bracket is
+// -g - g_H (ln p + H). Elementwise once the row's sums are known, so the row
+// is cut into pieces of kGradThreads * kGradAhead vectors, a CTA each.
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(GradArgs a) {
+  constexpr int E = Vec<T>::kLen;
+  const int row = blockIdx.x / a.pieces, piece = blockIdx.x - row * a.pieces, tid = threadIdx.x, V = a.V;
+  const Row<T> r(static_cast<const T*>(a.logits) + row * a.stride, V);
   T* d = static_cast<T*>(a.dlogits) + row * a.gstride;
-  const int tok = a.tokens[row];
-  const float m = a.stats[2ll * row], s = a.stats[2ll * row + 1];
-  if (tid == 0 && (tok < -1 || tok >= V))
-    set_error(a.err, DSPARK_ERR_DEVICE_ASSERT, 0x70000000u | static_cast<unsigned>(row));
-  if (tok < 0 || tok >= V || m == -INFINITY) {
-    for (int v = tid; v < V; v += kThreads) store(d + v, 0.f);
-    return;
+  const uint4* vecs = r.vecs();
+  uint4* dvecs = reinterpret_cast<uint4*>(d + r.head);
+  const int i0 = piece * kGradThreads * kGradAhead + tid;
+  uint4 v[kGradAhead];
+  if (kVec) {
+#pragma unroll
+    for (int u = 0; u < kGradAhead; ++u)
+      if (i0 + u * kGradThreads < r.nvec) v[u] = __ldcs(vecs + i0 + u * kGradThreads);
   }
-  // p = 2^y f, ln p = y ln 2 + lf
-  const float f = 1.f / s;
-  const float lf = static_cast<float>(-log(static_cast<double>(s)));
+  const int tok = a.tokens[row];
+  const float2 st = reinterpret_cast<const float2*>(a.stats)[row];
   const float g = a.g_logprob[row];
-  const float gh = a.g_entropy != nullptr ? a.g_entropy[row] : 0.f;
-  const float c0 = -g - (a.g_entropy != nullptr ? gh * (lf + a.entropy[row]) : 0.f);
-  const float c1 = -gh * static_cast<float>(kLn2);
-  for (int v = tid; v < V; v += kThreads) {
-    const float xv = to_float(x[v]);
-    const float y = fmax_nan((xv - m) * kLog2e, kMinExp);
-    const float p = exp2f(y) * f;
-    float dv = p * fmaf(c1, y, c0);
-    if (v == tok && xv != -INFINITY) dv += g;
-    store(d + v, dv);
+  if (tid == 0 && piece == 0 && (tok < -1 || tok >= V))
+    set_error(a.err, DSPARK_ERR_DEVICE_ASSERT, 0x70000000u | static_cast<unsigned>(row));
+  const bool none = tok < 0 || tok >= V || st.x == -INFINITY;
+  const float f = 1.f / st.y, lf = -logf(st.y);
+  float c0 = -g, c1 = 0.f;
+  if (a.g_entropy != nullptr) {
+    const float gh = a.g_entropy[row];
+    c0 -= gh * (lf + a.entropy[row]);
+    c1 = -gh * static_cast<float>(kLn2);
+  }
+  const float m = st.x;
+  auto one = [&](float x, int v) {
+    const float y = fmax_nan((x - m) * kLog2e, kMinExp);
+    float dv = ex2(y) * f * fmaf(c1, y, c0);
+    if (v == tok && x != -INFINITY) dv += g;
+    return none ? 0.f : dv;
+  };
+  if constexpr (!kVec) {     // rows and gradients aligned differently: element by element
+    constexpr int kPer = kGradAhead * E;
+    const int e0 = piece * kGradThreads * kPer + tid;
+#pragma unroll 4
+    for (int u = 0; u < kPer; ++u) {
+      const int e = e0 + u * kGradThreads;
+      if (e < V) store(d + e, one(to_float(r.x[e]), e));
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < kGradAhead; ++u) {
+      const int i = i0 + u * kGradThreads;
+      if (i < r.nvec) {
+        F2 q[E / 2];
+#pragma unroll
+        for (int j = 0; j < E / 2; ++j) {
+          const F2 x = Vec<T>::pair(v[u], j);
+          const int e = r.head + i * E + 2 * j;
+          q[j] = f2(one(f2_lo(x), e), one(f2_hi(x), e + 1));
+        }
+        __stcs(dvecs + i, Vec<T>::pack(q));
+      }
+    }
+    if (piece == a.pieces - 1 && tid < r.head + r.tail) {
+      const int e = tid < r.head ? tid : V - r.tail + tid - r.head;
+      store(d + e, one(to_float(r.x[e]), e));
+    }
   }
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool given(const void* p) { return p != nullptr && aligned16(p); }
+
+template <typename T>
+cudaError_t launch_logprobs(ScoreArgs a, int items, cudaStream_t s) {
+  constexpr int E = Vec<T>::kLen;
+  const int tiles = std::max(1, (a.V / E + kTile - 1) / kTile);
+  // few rows: a row is shared by up to 8 CTAs (a portable cluster), while that
+  // leaves each CTA eight tiles or more
+  int parts = 1;
+  while (parts < 8 && static_cast<long long>(items) * parts < 4 * kSms && tiles / (2 * parts) >= 8) parts *= 2;
+  const int most = (tiles + parts - 1) / parts;
+  a.parts = parts;
+  a.group = (most + kMaxSegs - 1) / kMaxSegs;
+  a.room = 32 + std::max(32 * E, std::min(kRoom, most * kTile * E));
+  const int warps = std::min(most, kMaxWarps);
+  const bool top = a.top_k > 0;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(items) * parts);
+  cfg.blockDim = dim3(warps * 32);
+  cfg.dynamicSmemBytes = top ? a.room * sizeof(unsigned long long) : 0;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = parts;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = parts > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, top ? logprobs_kernel<T, true> : logprobs_kernel<T, false>, a);
+}
+
+template <typename T>
+cudaError_t launch_grad(GradArgs a, int N, cudaStream_t s) {
+  constexpr int E = Vec<T>::kLen;
+  const int per = kGradThreads * kGradAhead * E;
+  a.pieces = (a.V + per - 1) / per;
+  if (static_cast<long long>(N) * a.pieces > 0x7fffffffll) return cudaErrorInvalidValue;
+  // vectors if every row's gradient has the row's own alignment
+  const bool vec = (a.stride - a.gstride) % E == 0;
+  (vec ? logprobs_grad_kernel<T, true> : logprobs_grad_kernel<T, false>)<<<N * a.pieces, kGradThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
 
 }  // namespace
 }  // namespace dspark
@@ -206,14 +657,11 @@ dspark_status dspark_logprobs(const void* logits, dspark_dtype dtype, int64_t n_
   if (!aligned16(row_start) || !aligned16(entropy) || !aligned16(stats)) return DSPARK_ERR_INVALID_ARG;
   if (top_k > 0 && (!given(top_tokens) || !given(top_logprobs))) return DSPARK_ERR_INVALID_ARG;
   if (ws_bytes < kScratchOffset) return DSPARK_ERR_INVALID_ARG;
-  const ScoreArgs a{logits, n_rows, row_stride, row_start, tokens, C, V, top_k, logprob, entropy, stats, top_tokens,
-                    top_logprobs, reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + kErrOffset)};
+  ScoreArgs a{logits, n_rows, row_stride, row_start, tokens, C, V, top_k, logprob, entropy, stats, top_tokens,
+              top_logprobs, reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + kErrOffset), 1, 1, 0};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == DSPARK_F32)
-    logprobs_kernel<float><<<B * C, kThreads, 0, s>>>(a);
-  else
-    logprobs_kernel<uint16_t><<<B * C, kThreads, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  const cudaError_t e = dtype == DSPARK_F32 ? launch_logprobs<float>(a, B * C, s) : launch_logprobs<uint16_t>(a, B * C, s);
+  return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 dspark_status dspark_logprobs_grad(const void* logits, dspark_dtype dtype, int64_t row_stride,
@@ -230,14 +678,11 @@ dspark_status dspark_logprobs_grad(const void* logits, dspark_dtype dtype, int64
   if (g_entropy != nullptr && (!given(g_entropy) || !given(entropy))) return DSPARK_ERR_INVALID_ARG;
   if (dlogits == logits && row_stride != grad_stride) return DSPARK_ERR_INVALID_ARG;
   if (ws_bytes < kScratchOffset) return DSPARK_ERR_INVALID_ARG;
-  const GradArgs a{logits, row_stride, grad_stride, tokens, stats, entropy, g_logprob, g_entropy, V, dlogits,
-                   reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + kErrOffset)};
+  GradArgs a{logits, row_stride, grad_stride, tokens, stats, entropy, g_logprob, g_entropy, V, dlogits,
+             reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + kErrOffset), 1};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == DSPARK_F32)
-    logprobs_grad_kernel<float><<<N, kThreads, 0, s>>>(a);
-  else
-    logprobs_grad_kernel<uint16_t><<<N, kThreads, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  const cudaError_t e = dtype == DSPARK_F32 ? launch_grad<float>(a, N, s) : launch_grad<uint16_t>(a, N, s);
+  return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 }  // extern "C"
