@@ -36,7 +36,7 @@ struct ScoreArgs {
   float* top_logprobs;
   unsigned* err;
   int parts;   // CTAs of a cluster, each with an equal part of the row
-  int group;   // tiles of a segment (alternatives)
+  int group;   // rows of 32 vectors of a segment (alternatives): 1, or a multiple of kAhead
   int room;    // candidates that shared memory holds
 };
 
@@ -319,8 +319,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) logprobs_kernel(ScoreArgs a
   const int tiles = (r.nvec + kTile - 1) / kTile;
   const int t0 = static_cast<int>(static_cast<long long>(tiles) * part / parts);
   const int t1 = static_cast<int>(static_cast<long long>(tiles) * (part + 1) / parts);
-  const int segs = (t1 - t0 + a.group - 1) / a.group;
-  if (kTop && a.group > 1) {
+  const int segs = ((t1 - t0) * kAhead + a.group - 1) / a.group;
+  if (kTop && a.group > kAhead) {
     for (int i = tid; i < segs; i += nt) s_seg[i] = 0u;
     __syncthreads();
   }
@@ -335,20 +335,30 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) logprobs_kernel(ScoreArgs a
       const unsigned ni = Vec<T>::kNegInf;
       v[u] = i0 + u * 32 < r.nvec ? __ldg(vecs + i0 + u * 32) : make_uint4(ni, ni, ni, ni);
     }
-    float most = Vec<T>::largest(v[0]);
+    float most = -INFINITY;
+    if (kTop && a.group == 1) {
 #pragma unroll
-    for (int u = 1; u < kAhead; ++u) most = fmaxf(most, Vec<T>::largest(v[u]));
-    raise(m, S, Tsum, most);
-    add_terms<T>(v, m, S, Tsum);
-    if (kTop) {
-      const unsigned o = __reduce_max_sync(0xffffffffu, order_of(fmaxf(most, -INFINITY)));
-      if (lane == 0) {
-        if (a.group == 1)
-          s_seg[t - t0] = o;
-        else
-          atomicMax(&s_seg[(t - t0) / a.group], o);
+      for (int u = 0; u < kAhead; ++u) {
+        const float here = Vec<T>::largest(v[u]);
+        const unsigned o = __reduce_max_sync(0xffffffffu, order_of(fmaxf(here, -INFINITY)));
+        if (lane == 0) s_seg[(t - t0) * kAhead + u] = o;
+        most = fmaxf(most, here);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) most = fmaxf(most, Vec<T>::largest(v[u]));
+      if (kTop) {
+        const unsigned o = __reduce_max_sync(0xffffffffu, order_of(fmaxf(most, -INFINITY)));
+        if (lane == 0) {
+          if (a.group == kAhead)
+            s_seg[t - t0] = o;
+          else
+            atomicMax(&s_seg[(t - t0) * kAhead / a.group], o);
+        }
       }
     }
+    raise(m, S, Tsum, most);
+    add_terms<T>(v, m, S, Tsum);
   }
   // the ends outside the vectors: at most kLen - 1 elements each
   const int ends = (part == 0 ? r.head : 0) + (part == parts - 1 ? r.tail : 0);
@@ -400,11 +410,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) logprobs_kernel(ScoreArgs a
     __syncthreads();
     // below tau there is nothing to find; -inf is never a candidate
     const float tau = segs >= k ? order_value(s_tau) : -INFINITY;
-    const int units = chosen * a.group * kAhead;       // rows of 32 vectors
+    const int units = chosen * a.group;                // rows of 32 vectors
     auto vec_of = [&](int unit) {                      // the lane's vector, -1: none
-      const int tile = t0 + s_chosen[unit / (a.group * kAhead)] * a.group + unit / kAhead % a.group;
-      const int i = tile * kTile + unit % kAhead * 32 + lane;
-      return tile < t1 && i < r.nvec ? i : -1;
+      const int at = t0 * kAhead + s_chosen[unit / a.group] * a.group + unit % a.group;
+      const int i = at * 32 + lane;
+      return at < t1 * kAhead && i < r.nvec ? i : -1;
     };
     auto offer = [&](float x, int v, unsigned long long above, int room) {
       if (!(x >= tau) || x == -INFINITY) return;
@@ -607,7 +617,9 @@ cudaError_t launch_logprobs(ScoreArgs a, int items, cudaStream_t s) {
   while (parts < 8 && static_cast<long long>(items) * parts < 4 * kSms && tiles / (2 * parts) >= 8) parts *= 2;
   const int most = (tiles + parts - 1) / parts;
   a.parts = parts;
-  a.group = (most + kMaxSegs - 1) / kMaxSegs;
+  // segments of one row of 32 vectors while shared memory holds so many, else
+  // of whole tiles: fewer maxima to note (one a tile), more to read again
+  a.group = most * kAhead <= kMaxSegs ? 1 : (most + kMaxSegs - 1) / kMaxSegs * kAhead;
   a.room = 32 + std::max(32 * E, std::min(kRoom, most * kTile * E));
   const int warps = std::min(most, kMaxWarps);
   const bool top = a.top_k > 0;
