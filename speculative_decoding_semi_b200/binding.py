@@ -292,9 +292,10 @@ _DTYPES = {torch.float32: DSPARK_F32, torch.bfloat16: DSPARK_BF16}
 def _dtype(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype not in _DTYPES:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
-    return _DTYPES[t.dtype]
+    return code
 
 
 def _rows(t: torch.Tensor, name: str) -> tuple[int, int, int, int]:
@@ -314,27 +315,32 @@ def _rows(t: torch.Tensor, name: str) -> tuple[int, int, int, int]:
 
 
 def _on(dev: int, t: torch.Tensor | None, name: str, dtype, numel: int) -> int | None:
-    """_ptr for a tensor that has to be on device `dev`; the calls of a small
-    batch are bound by the time spent here, so the good case is one line."""
+    """_ptr for a tensor that has to be on device `dev`. The calls of a small
+    batch are bound by the time spent here, so the good case comes first."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.numel() == numel \
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.numel() == numel \
             and t.is_contiguous():
         return t.data_ptr()
     _ptr(t, name, dtype, numel)
     raise ValueError(f"{name}: expected a tensor on cuda:{dev}, got {t.device}")
 
 
-def _call(name: str, dev: int, stream, *args) -> None:
-    """The C call with the tensors' device current, so that the launch and the
-    default stream are that device's."""
+def _launch_stream(name: str, dev: int, stream) -> int | None:
+    """The stream's handle; None where the tensors' device is not the current
+    one (the call is then made with it current)."""
     if dev < 0:
         raise ValueError(f"{name}: expected CUDA tensors (the library computes on the GPU only)")
-    fn = getattr(lib, name)
-    if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
+    if stream is not None and isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
         raise ValueError(f"{name}: tensors on cuda:{dev}, stream on {stream.device}")
-    if dev == torch.cuda.current_device():
-        s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if dev != torch._C._cuda_getDevice():
+        return None
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _call(fn, name: str, dev: int, stream, *args) -> None:
+    s = _launch_stream(name, dev, stream)
+    if s is not None:
         status = fn(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -361,16 +367,13 @@ def dspark_logprobs(logits, tokens, logprob, entropy, stats, top_tokens, top_log
             raise ValueError("top_tokens: expected [B,C,top_k]")
         k = top_tokens.shape[2]
     f32, i32 = torch.float32, torch.int32
-    _call("dspark_logprobs", dev, stream, ptr, dt, n_rows, ld, _on(dev, row_start, "row_start", torch.int64, B),
-          _on(dev, tokens, "tokens", i32, n), B, C, V, k, _on(dev, logprob, "logprob", f32, n),
-          _on(dev, entropy, "entropy", f32, n), _on(dev, stats, "stats", f32, 2 * n),
-          _on(dev, top_tokens, "top_tokens", i32, n * k), _on(dev, top_logprobs, "top_logprobs", f32, n * k),
-          *_workspace(dev, workspace))
-
-
-def _workspace(dev: int, workspace: torch.Tensor) -> tuple[int, int]:
     size = workspace.numel()
-    return _on(dev, workspace, "workspace", torch.uint8, size), size
+    _call(lib.dspark_logprobs, "dspark_logprobs", dev, stream, ptr, dt, n_rows, ld,
+          _on(dev, row_start, "row_start", torch.int64, B), _on(dev, tokens, "tokens", i32, n), B, C, V, k,
+          _on(dev, logprob, "logprob", f32, n), _on(dev, entropy, "entropy", f32, n),
+          _on(dev, stats, "stats", f32, 2 * n), _on(dev, top_tokens, "top_tokens", i32, n * k),
+          _on(dev, top_logprobs, "top_logprobs", f32, n * k), _on(dev, workspace, "workspace", torch.uint8, size),
+          size)
 
 
 def dspark_logprobs_grad(logits, tokens, stats, entropy, g_logprob, g_entropy, dlogits, workspace,
@@ -379,7 +382,7 @@ def dspark_logprobs_grad(logits, tokens, stats, entropy, g_logprob, g_entropy, d
     g_logprob [N]) and entropy (times g_entropy [N], or None) with respect to
     logits [N,V]; tokens [N] or any shape of N elements. dlogits may be logits."""
     dt = _dtype(logits, "logits")
-    if _dtype(dlogits, "dlogits") != dt:
+    if dlogits.dtype is not logits.dtype:
         raise TypeError("dlogits: expected the type of logits")
     ptr, N, V, ld = _rows(logits, "logits")
     gptr, gN, gV, gld = _rows(dlogits, "dlogits")
@@ -387,13 +390,28 @@ def dspark_logprobs_grad(logits, tokens, stats, entropy, g_logprob, g_entropy, d
         raise ValueError(f"dlogits: expected [{N},{V}], got [{gN},{gV}]")
     if g_entropy is not None and entropy is None:
         raise ValueError("entropy: needed with g_entropy")
-    dev, f32 = logits.get_device(), torch.float32
+    dev, f32, size = logits.get_device(), torch.float32, workspace.numel()
     if dlogits.get_device() != dev:
         raise ValueError(f"dlogits: expected a tensor on cuda:{dev}, got {dlogits.device}")
-    _call("dspark_logprobs_grad", dev, stream, ptr, dt, ld, _on(dev, tokens, "tokens", torch.int32, N),
-          _on(dev, stats, "stats", f32, 2 * N), _on(dev, entropy, "entropy", f32, N),
-          _on(dev, g_logprob, "g_logprob", f32, N), _on(dev, g_entropy, "g_entropy", f32, N), N, V, gptr, gld,
-          *_workspace(dev, workspace))
+    _call(lib.dspark_logprobs_grad, "dspark_logprobs_grad", dev, stream, ptr, dt, ld,
+          _on(dev, tokens, "tokens", torch.int32, N), _on(dev, stats, "stats", f32, 2 * N),
+          _on(dev, entropy, "entropy", f32, N), _on(dev, g_logprob, "g_logprob", f32, N),
+          _on(dev, g_entropy, "g_entropy", f32, N), N, V, gptr, gld,
+          _on(dev, workspace, "workspace", torch.uint8, size), size)
+
+
+def _embed_ptrs(dev: int, table, tokens, rows, name: str, workspace, n: int, V: int, r: int):
+    """Pointers of a table [V,r], tokens [n], rows [n,r] (called `name`) and
+    the workspace, all on device `dev`; one look at each tensor's properties."""
+    size = workspace.numel()
+    if (table.is_contiguous() and rows.is_contiguous() and tokens.is_contiguous() and workspace.is_contiguous()
+            and tokens.dtype is torch.int32 and workspace.dtype is torch.uint8 and rows.numel() == n * r
+            and tokens.get_device() == rows.get_device() == workspace.get_device() == dev):
+        return table.data_ptr(), tokens.data_ptr(), rows.data_ptr(), workspace.data_ptr(), size
+    _dtype(rows, name)      # say what is wrong
+    return (_on(dev, table, "table" if name == "out" else "dtable", table.dtype, V * r),
+            _on(dev, tokens, "tokens", torch.int32, n), _on(dev, rows, name, rows.dtype, n * r),
+            _on(dev, workspace, "workspace", torch.uint8, size), size)
 
 
 def dspark_embed(table, tokens, scale: float, out, workspace, stream=None) -> None:
@@ -401,9 +419,9 @@ def dspark_embed(table, tokens, scale: float, out, workspace, stream=None) -> No
     and out each float32 or bfloat16."""
     V, r = table.shape
     n, dev = tokens.numel(), table.get_device()
-    _call("dspark_embed", dev, stream, _on(dev, table, "table", table.dtype, V * r), _dtype(table, "table"),
-          _on(dev, tokens, "tokens", torch.int32, n), n, V, r, scale, _on(dev, out, "out", out.dtype, n * r),
-          _dtype(out, "out"), *_workspace(dev, workspace))
+    t, tok, o, ws, size = _embed_ptrs(dev, table, tokens, out, "out", workspace, n, V, r)
+    _call(lib.dspark_embed, "dspark_embed", dev, stream, t, _dtype(table, "table"), tok, n, V, r, scale, o,
+          _dtype(out, "out"), ws, size)
 
 
 def dspark_embed_grad_workspace_bytes(n: int, V: int, r: int) -> int:
@@ -418,9 +436,9 @@ def dspark_embed_grad(dout, tokens, scale: float, dtable, workspace, accumulate:
     the items of each token; dout and dtable each float32 or bfloat16."""
     V, r = dtable.shape
     n, dev = tokens.numel(), dtable.get_device()
-    _call("dspark_embed_grad", dev, stream, _on(dev, dout, "dout", dout.dtype, n * r), _dtype(dout, "dout"),
-          _on(dev, tokens, "tokens", torch.int32, n), n, V, r, scale, 1 if accumulate else 0,
-          _on(dev, dtable, "dtable", dtable.dtype, V * r), _dtype(dtable, "dtable"), *_workspace(dev, workspace))
+    d, tok, o, ws, size = _embed_ptrs(dev, dtable, tokens, dout, "dout", workspace, n, V, r)
+    _call(lib.dspark_embed_grad, "dspark_embed_grad", dev, stream, o, _dtype(dout, "dout"), tok, n, V, r, scale,
+          1 if accumulate else 0, d, _dtype(dtable, "dtable"), ws, size)
 
 
 DSPARK_INJECT_NONE, DSPARK_INJECT_DRAFT_SLICE_SUMS, DSPARK_INJECT_VERIFY_BARRIER = 0, 1, 2

@@ -87,6 +87,13 @@ struct Vec<float> {
     return make_uint4(__float_as_uint(f2_lo(d[0])), __float_as_uint(f2_hi(d[0])), __float_as_uint(f2_lo(d[1])),
                       __float_as_uint(f2_hi(d[1])));
   }
+  // the elements, none below -1e38 (near terms: y stays finite, 2^y is 0)
+  __device__ __forceinline__ static uint4 floor(const uint4& v) {
+    return make_uint4(__float_as_uint(fmax_nan(__uint_as_float(v.x), -1e38f)),
+                      __float_as_uint(fmax_nan(__uint_as_float(v.y), -1e38f)),
+                      __float_as_uint(fmax_nan(__uint_as_float(v.z), -1e38f)),
+                      __float_as_uint(fmax_nan(__uint_as_float(v.w), -1e38f)));
+  }
   __device__ __forceinline__ static float largest(const uint4& v) {
     return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
   }
@@ -106,6 +113,15 @@ struct Vec<uint16_t> {
   __device__ __forceinline__ static unsigned max2(unsigned a, unsigned b) {   // NaN gives way
     unsigned d;
     asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  __device__ __forceinline__ static uint4 floor(const uint4& v) {
+    constexpr unsigned kLow = 0xfe96fe96u;   // -1e38
+    uint4 d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d.x) : "r"(v.x), "r"(kLow));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d.y) : "r"(v.y), "r"(kLow));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d.z) : "r"(v.z), "r"(kLow));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d.w) : "r"(v.w), "r"(kLow));
     return d;
   }
   __device__ __forceinline__ static float largest(const uint4& v) {
@@ -132,66 +148,81 @@ struct Row {
 
 // --------------------------------------------------------------- scores
 
-constexpr int kAhead = 8;                 // vectors of a lane in flight
+constexpr int kAhead = 4;                 // vectors of a lane in flight
 constexpr int kTile = 32 * kAhead;        // vectors of a tile: one warp, one step
-constexpr int kMaxWarps = 16;
+constexpr int kMaxWarps = 8;
 constexpr int kMaxSegs = 256;             // segments of a CTA's part
+constexpr float kSlack = 4.f;             // how far logits may exceed the sums' c before it is raised
 constexpr int kRoom = 2048;               // candidates beside the top_k that are kept
 
-// Largest logit, sum and tilted sum of some elements of a row.
-struct Triple {
-  float m;
+// Sum and tilted sum of some elements of a row with the shift of a logit c
+// near their largest: S = sum 2^y, T = sum y 2^y, y = x log2 e - shift2(c);
+// c = -inf: no finite element, S and T are 0 (or NaN).
+struct Sums {
+  float c;
   double S, T;
 };
 
-__device__ __forceinline__ Triple join(const Triple& a, const Triple& b) {
-  Triple r;
-  r.m = fmaxf(a.m, b.m);
-  if (r.m == -INFINITY) {       // no finite element: S and T are 0 or NaN
-    r.S = a.S + b.S;
-    r.T = a.T + b.T;
-    return r;
-  }
-  // an empty side (m = -inf) has S = T = 0, or NaN
-  const float da = a.m == -INFINITY ? 0.f : (r.m - a.m) * kLog2e, db = b.m == -INFINITY ? 0.f : (r.m - b.m) * kLog2e;
-  const double fa = ex2(-da), fb = ex2(-db);
-  r.S = a.S * fa + b.S * fb;
-  r.T = (fa > 0.0 ? (a.T - da * a.S) * fa : a.S * 0.0) + (fb > 0.0 ? (b.T - db * b.S) * fb : b.S * 0.0);
-  return r;
+// Up to kNear the terms take one fused step, y = fl(x log2 e - h) with
+// h = fl(c log2 e): h is the same number in every term, so its rounding (at
+// most 2^-7 there) cancels, and the sum's shift is h. Beyond, the difference
+// x - c is taken first.
+constexpr float kNear = 65536.f;
+__device__ __forceinline__ bool is_near(float c) { return fabsf(c) < kNear; }
+__device__ __forceinline__ double shift2(float c) {
+  return is_near(c) ? static_cast<double>(c * kLog2e) : static_cast<double>(c) * kLog2e;
 }
 
-// Adds the kCount vectors v to the lane's triple, whose m is at least as large
-// as every element; sums of at most 64 terms are fp32.
-template <typename T, int kCount>
-__device__ __forceinline__ void add_terms(const uint4 (&v)[kCount], float m, double& S, double& Tsum) {
-  const float shift = m == -INFINITY ? 0.f : m;
-  const F2 ns = f2(-shift, -shift), l2e = f2(kLog2e, kLog2e);
-  F2 s = f2(0.f, 0.f), t = f2(0.f, 0.f);
-#pragma unroll
-  for (int k = 0; k < kCount; ++k) {
-#pragma unroll
-    for (int j = 0; j < Vec<T>::kLen / 2; ++j) {
-      const F2 y0 = mul2(add2(Vec<T>::pair(v[k], j), ns), l2e);
-      const F2 y = f2(fmax_nan(f2_lo(y0), kMinExp), fmax_nan(f2_hi(y0), kMinExp));
-      const F2 e = f2(ex2(f2_lo(y)), ex2(f2_hi(y)));
-      s = add2(s, e);
-      t = fma2(e, y, t);
-    }
-  }
-  S += static_cast<double>(f2_lo(s)) + static_cast<double>(f2_hi(s));
-  Tsum += static_cast<double>(f2_lo(t)) + static_cast<double>(f2_hi(t));
-}
-
-// Moves a triple to a larger m.
-__device__ __forceinline__ void raise(float& m, double& S, double& Tsum, float to) {
-  if (!(to > m)) return;
-  if (m != -INFINITY) {
-    const float d = (to - m) * kLog2e;
+// Moves the sums to a larger c.
+__device__ __forceinline__ void raise(Sums& s, float to) {
+  if (!(to > s.c)) return;
+  if (s.c != -INFINITY) {
+    const float d = static_cast<float>(shift2(to) - shift2(s.c));
     const double f = ex2(-d);
-    Tsum = f > 0.0 ? (Tsum - d * S) * f : S * 0.0;
-    S *= f;
+    s.T = f > 0.0 ? (s.T - d * s.S) * f : s.S * 0.0;
+    s.S *= f;
   }
-  m = to;
+  s.c = to;
+}
+
+__device__ __forceinline__ Sums join(Sums a, Sums b) {
+  raise(a, b.c);
+  raise(b, a.c);
+  return Sums{a.c, a.S + b.S, a.T + b.T};
+}
+
+// Adds the kCount vectors v to a lane's sums; up to 64 terms are added in fp32.
+template <typename T, int kCount>
+__device__ __forceinline__ void add_terms(const uint4 (&v)[kCount], Sums& sums) {
+  const bool near = is_near(sums.c);
+  const float h = sums.c * kLog2e, shift = sums.c == -INFINITY ? 0.f : sums.c;
+  F2 s = f2(0.f, 0.f), t = f2(0.f, 0.f);
+  if (near) {
+#pragma unroll
+    for (int k = 0; k < kCount; ++k) {
+      const uint4 c = Vec<T>::floor(v[k]);
+#pragma unroll
+      for (int j = 0; j < Vec<T>::kLen / 2; ++j) {
+        const F2 y = fma2(Vec<T>::pair(c, j), f2(kLog2e, kLog2e), f2(-h, -h));
+        const F2 e = f2(ex2(f2_lo(y)), ex2(f2_hi(y)));
+        s = add2(s, e);
+        t = fma2(e, y, t);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kCount; ++k)
+#pragma unroll
+      for (int j = 0; j < Vec<T>::kLen / 2; ++j) {
+        const F2 x = Vec<T>::pair(v[k], j);
+        const F2 y = f2(fmax_nan((f2_lo(x) - shift) * kLog2e, kMinExp), fmax_nan((f2_hi(x) - shift) * kLog2e, kMinExp));
+        const F2 e = f2(ex2(f2_lo(y)), ex2(f2_hi(y)));
+        s = add2(s, e);
+        t = fma2(e, y, t);
+      }
+  }
+  sums.S += static_cast<double>(f2_lo(s) + f2_hi(s));
+  sums.T += static_cast<double>(f2_lo(t) + f2_hi(t));
 }
 
 // The alternatives' order as one number: the logit's order (-0 as 0), then the
@@ -278,7 +309,7 @@ __device__ __forceinline__ unsigned long long read_peer(const void* p, int rank)
 // row notes the segments' maxima only; the chosen segments are read again for
 // the elements that reach the last one's maximum.
 template <typename T, bool kTop>
-__global__ void __launch_bounds__(kMaxWarps * 32, 2) logprobs_kernel(ScoreArgs a) {
+__global__ void __launch_bounds__(kMaxWarps * 32, 4) logprobs_kernel(ScoreArgs a) {
   constexpr int E = Vec<T>::kLen;
   extern __shared__ unsigned long long s_keys[];        // [room]
   __shared__ unsigned s_seg[kTop ? kMaxSegs : 1];
@@ -286,9 +317,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) logprobs_kernel(ScoreArgs a
   __shared__ unsigned long long s_top[32];
   __shared__ int s_count;
   __shared__ unsigned s_tau;
-  __shared__ double s_S[kMaxWarps], s_T[kMaxWarps];
+  __shared__ Sums s_sums[kMaxWarps];
   __shared__ float s_m[kMaxWarps];
-  __shared__ unsigned long long s_mine[3];              // the CTA's triple, for the cluster
+  __shared__ double s_lse[2];
+  __shared__ unsigned long long s_mine[3];              // the CTA's largest logit and sums, for the cluster
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, nt = blockDim.x, W = nt >> 5;
   const int parts = a.parts, part = parts > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int item = blockIdx.x / parts, V = a.V, k = a.top_k;
@@ -325,16 +357,23 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) logprobs_kernel(ScoreArgs a
     __syncthreads();
   }
 
-  float m = -INFINITY;
-  double S = 0.0, Tsum = 0.0;
-  for (int t = t0 + w; t < t1; t += W) {
-    uint4 v[kAhead];
+  float m = -INFINITY;                     // the lane's largest logit
+  Sums sums{-INFINITY, 0.0, 0.0};          // c is the warp's: the largest logit when it was set
+  auto load = [&](uint4 (&v)[kAhead], int t) {
     const int i0 = t * kTile + lane;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const unsigned ni = Vec<T>::kNegInf;
       v[u] = i0 + u * 32 < r.nvec ? __ldg(vecs + i0 + u * 32) : make_uint4(ni, ni, ni, ni);
     }
+  };
+  uint4 next[kAhead];
+  if (t0 + w < t1) load(next, t0 + w);
+  for (int t = t0 + w; t < t1; t += W) {
+    uint4 v[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) v[u] = next[u];
+    if (t + W < t1) load(next, t + W);
     float most = -INFINITY;
     if (kTop && a.group == 1) {
 #pragma unroll
@@ -348,7 +387,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) logprobs_kernel(ScoreArgs a
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) most = fmaxf(most, Vec<T>::largest(v[u]));
       if (kTop) {
-        const unsigned o = __reduce_max_sync(0xffffffffu, order_of(fmaxf(most, -INFINITY)));
+        const unsigned o = __reduce_max_sync(0xffffffffu, order_of(most));
         if (lane == 0) {
           if (a.group == kAhead)
             s_seg[t - t0] = o;
@@ -357,42 +396,47 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) logprobs_kernel(ScoreArgs a
         }
       }
     }
-    raise(m, S, Tsum, most);
-    add_terms<T>(v, m, S, Tsum);
+    m = fmaxf(m, most);
+    if (__any_sync(0xffffffffu, most > sums.c + kSlack))      // rare behind the first tile
+      raise(sums, order_value(__reduce_max_sync(0xffffffffu, order_of(most))));
+    add_terms<T>(v, sums);
   }
   // the ends outside the vectors: at most kLen - 1 elements each
   const int ends = (part == 0 ? r.head : 0) + (part == parts - 1 ? r.tail : 0);
   int end_at = -1;
   float end_x = -INFINITY;
-  if (w == 0 && lane < ends) {
-    end_at = part == 0 && lane < r.head ? lane : V - ends + lane;
-    end_x = to_float(r.x[end_at]);
-    raise(m, S, Tsum, end_x);
-    const float y = fmax_nan((end_x - (m == -INFINITY ? 0.f : m)) * kLog2e, kMinExp), e = ex2(y);
-    S += e;
-    Tsum += static_cast<double>(e * y);
+  if (w == 0 && ends > 0) {
+    if (lane < ends) {
+      end_at = part == 0 && lane < r.head ? lane : V - ends + lane;
+      end_x = to_float(r.x[end_at]);
+    }
+    m = fmaxf(m, end_x);
+    raise(sums, order_value(__reduce_max_sync(0xffffffffu, order_of(m))));
+    if (lane < ends) {
+      const float c = sums.c == -INFINITY ? 0.f : sums.c;
+      const float y = fmax_nan(is_near(c) ? fmaf(end_x, kLog2e, -(c * kLog2e)) : (end_x - c) * kLog2e, kMinExp);
+      const float e = ex2(y);
+      sums.S += e;
+      sums.T += static_cast<double>(e * y);
+    }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Triple other{__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, S, o),
-                       __shfl_xor_sync(0xffffffffu, Tsum, o)};
-    const Triple own{m, S, Tsum};
-    const Triple j = (lane & o) ? join(other, own) : join(own, other);
-    m = j.m;
-    S = j.S;
-    Tsum = j.T;
-  }
+  m = order_value(__reduce_max_sync(0xffffffffu, order_of(m)));
+  sums.S = warp_sum(sums.S);
+  sums.T = warp_sum(sums.T);
   if (lane == 0) {
     s_m[w] = m;
-    s_S[w] = S;
-    s_T[w] = Tsum;
+    s_sums[w] = sums;
   }
   if (tid == 0) s_count = 0;
   __syncthreads();
-  Triple all{s_m[0], s_S[0], s_T[0]};
+  Sums all = s_sums[0];
+  m = s_m[0];
   if (tid == 0) {
-    for (int j = 1; j < W; ++j) all = join(all, Triple{s_m[j], s_S[j], s_T[j]});
-    s_mine[0] = __float_as_uint(all.m);
+    for (int j = 1; j < W; ++j) {
+      all = join(all, s_sums[j]);
+      m = fmaxf(m, s_m[j]);
+    }
+    s_mine[0] = (static_cast<unsigned long long>(__float_as_uint(m)) << 32) | __float_as_uint(all.c);
     s_mine[1] = __double_as_longlong(all.S);
     s_mine[2] = __double_as_longlong(all.T);
   }
@@ -479,10 +523,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) logprobs_kernel(ScoreArgs a
     cluster_sync();
     if (part == 0) {
       if (tid == 0)
-        for (int p = 1; p < parts; ++p)
-          all = join(all, Triple{__uint_as_float(static_cast<unsigned>(read_peer(&s_mine[0], p))),
-                                 __longlong_as_double(read_peer(&s_mine[1], p)),
-                                 __longlong_as_double(read_peer(&s_mine[2], p))});
+        for (int p = 1; p < parts; ++p) {
+          const unsigned long long mc = read_peer(&s_mine[0], p);
+          m = fmaxf(m, __uint_as_float(static_cast<unsigned>(mc >> 32)));
+          all = join(all, Sums{__uint_as_float(static_cast<unsigned>(mc)), __longlong_as_double(read_peer(&s_mine[1], p)),
+                               __longlong_as_double(read_peer(&s_mine[2], p))});
+        }
       if (kTop) {
         if (tid == 0) s_count = 0;
         __syncthreads();
@@ -501,23 +547,27 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) logprobs_kernel(ScoreArgs a
   }
   const bool bad = !(all.S < 1e300);   // a NaN or +inf in the row
   if (tid == 0) {
-    const double shift = all.m == -INFINITY ? 0.0 : static_cast<double>(all.m), lnS = log(all.S);
-    float lp = xt == -INFINITY ? xt : static_cast<float>(static_cast<double>(xt) - shift - lnS);
-    float H = all.S > 0.0 ? static_cast<float>(lnS - kLn2 * (all.T / all.S)) : 0.f;
+    // ln sum e^(x - m), from the sum's own shift
+    const double top = m == -INFINITY ? 0.0 : static_cast<double>(m);
+    const double off = m == -INFINITY ? 0.0 : shift2(all.c) - top * kLog2e;
+    const double lnSum = log(all.S), lnS = lnSum + off * kLn2;
+    float lp = xt == -INFINITY ? xt : static_cast<float>(static_cast<double>(xt) - top - lnS);
+    float H = all.S > 0.0 ? static_cast<float>(lnSum - kLn2 * (all.T / all.S)) : 0.f;
     if (bad) lp = H = NAN;
     a.logprob[item] = lp;
     if (a.entropy != nullptr) a.entropy[item] = H;
     if (a.stats != nullptr)
-      reinterpret_cast<float2*>(a.stats)[item] = bad ? make_float2(NAN, NAN) : make_float2(all.m, static_cast<float>(all.S));
+      reinterpret_cast<float2*>(a.stats)[item] =
+          bad ? make_float2(NAN, NAN) : make_float2(m, static_cast<float>(all.S * exp2(off)));
     if (kTop) {
-      s_S[0] = shift;
-      s_T[0] = lnS;
+      s_lse[0] = top;
+      s_lse[1] = lnS;
       s_count = bad;
     }
   }
   if (kTop) {
     __syncthreads();
-    const double shift = s_S[0], lnS = s_T[0];
+    const double top = s_lse[0], lnS = s_lse[1];
     for (int i = tid; i < k; i += nt) {
       const unsigned long long key = s_top[i];
       const long long o = static_cast<long long>(item) * k + i;
@@ -525,7 +575,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) logprobs_kernel(ScoreArgs a
       a.top_tokens[o] = key != 0ull ? key_token(key) : -1;
       a.top_logprobs[o] = key == 0ull || s_count
                               ? none
-                              : static_cast<float>(order_value(static_cast<unsigned>(key >> 32)) - shift - lnS);
+                              : static_cast<float>(order_value(static_cast<unsigned>(key >> 32)) - top - lnS);
     }
   }
 }
