@@ -151,6 +151,7 @@ struct Row {
 constexpr int kAhead = 4;                 // vectors of a lane in flight
 constexpr int kTile = 32 * kAhead;        // vectors of a tile: one warp, one step
 constexpr int kMaxWarps = 8;
+constexpr int kMaxParts = 8;              // CTAs of a row (the portable cluster size)
 constexpr int kMaxSegs = 256;             // segments of a CTA's part
 constexpr float kSlack = 4.f;             // how far logits may exceed the sums' c before it is raised
 constexpr int kRoom = 2048;               // candidates beside the top_k that are kept
@@ -185,10 +186,18 @@ __device__ __forceinline__ void raise(Sums& s, float to) {
   s.c = to;
 }
 
-__device__ __forceinline__ Sums join(Sums a, Sums b) {
-  raise(a, b.c);
-  raise(b, a.c);
-  return Sums{a.c, a.S + b.S, a.T + b.T};
+// The sums of eight lanes, 0 to 7, in all of them.
+__device__ __forceinline__ Sums join8(Sums s) {
+  float c = s.c;
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, o));
+  raise(s, c);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    s.S += __shfl_xor_sync(0xffffffffu, s.S, o);
+    s.T += __shfl_xor_sync(0xffffffffu, s.T, o);
+  }
+  return s;
 }
 
 // Adds the kCount vectors v to a lane's sums; up to 64 terms are added in fp32.
@@ -241,45 +250,52 @@ __device__ __forceinline__ int key_token(unsigned long long k) {
   return static_cast<int>(0xffffffffu - static_cast<unsigned>(k));
 }
 
-// The k largest of n different keys, in order, to `out` (0 behind the n-th).
-// Few keys: each thread counts the keys above its own. Many: the k-th largest
-// is found bit by bit first, which leaves k. All threads of the CTA call.
-__device__ void take_largest(unsigned long long* keys, int n, int k, unsigned long long* out, int* s_count) {
-  const int tid = threadIdx.x, nt = blockDim.x;
-  if (n > 512) {
-    unsigned long long kth = 0ull;
-    for (int bit = 63; bit >= 0; --bit) {
-      const unsigned long long c = kth | (1ull << bit);
-      int mine = 0;
-      for (int i = tid; i < n; i += nt) mine += keys[i] >= c;
-      if (tid == 0) *s_count = 0;
-      __syncthreads();
-      mine = __reduce_add_sync(0xffffffffu, mine);
-      if ((tid & 31) == 0 && mine != 0) atomicAdd(s_count, mine);
-      __syncthreads();
-      const int above = *s_count;
-      __syncthreads();
-      if (above >= k) kth = c;
+// Descending order over a warp's lanes: a bitonic sort, and the 32 largest of
+// two sorted sets (the larger of one's i-th and the other's 31-i-th is a
+// bitonic sequence of them).
+__device__ __forceinline__ unsigned long long exchange(unsigned long long key, int distance, bool larger) {
+  const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, distance);
+  return (key > other) == larger ? key : other;
+}
+__device__ __forceinline__ unsigned long long clean32(unsigned long long key, int lane) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) key = exchange(key, d, (lane & d) == 0);
+  return key;
+}
+__device__ __forceinline__ unsigned long long sort32(unsigned long long key, int lane) {
+#pragma unroll
+  for (int size = 2; size < 32; size *= 2)
+#pragma unroll
+    for (int d = size / 2; d > 0; d >>= 1) key = exchange(key, d, ((lane & size) == 0) == ((lane & d) == 0));
+  return clean32(key, lane);
+}
+__device__ __forceinline__ unsigned long long merge32(unsigned long long a, unsigned long long b, int lane) {
+  b = __shfl_sync(0xffffffffu, b, 31 - lane);
+  return clean32(a > b ? a : b, lane);
+}
+
+// The 32 largest of n keys in order (0 behind the n-th) to warp 0's lanes and
+// to `out`: each warp sorts its share of the keys by 32, then the warps' best
+// are merged in pairs. All warps of the CTA call; `out` is ready when they
+// return. Keys are different, or 0.
+template <typename Key>
+__device__ __forceinline__ void take_largest(int n, Key key, unsigned long long (*s_best)[32], unsigned long long* out) {
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, W = blockDim.x >> 5;
+  const int busy = min(W, (n + 31) / 32);
+  unsigned long long best = 0ull;
+  for (int i = w * 32; i < n; i += W * 32) {
+    const unsigned long long more = sort32(i + lane < n ? key(i + lane) : 0ull, lane);
+    best = i == w * 32 ? more : merge32(best, more, lane);
+  }
+  if (w != 0 && w < busy) s_best[w][lane] = best;
+  for (int step = 1; step < busy; step *= 2) {
+    __syncthreads();
+    if (w % (2 * step) == 0 && w + step < busy) {
+      best = merge32(best, s_best[w + step][lane], lane);
+      if (w != 0) s_best[w][lane] = best;
     }
-    // n > 512 >= k keys, all different: exactly k are >= kth. They go to `out`
-    // in any order, then in order to the front of the list.
-    if (tid == 0) *s_count = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += nt)
-      if (keys[i] >= kth) out[atomicAdd(s_count, 1)] = keys[i];
-    __syncthreads();
-    for (int i = tid; i < k; i += nt) keys[i] = out[i];
-    n = k;
-    __syncthreads();
   }
-  for (int i = tid; i < k; i += nt)
-    if (i >= n) out[i] = 0ull;
-  for (int i = tid; i < n; i += nt) {
-    const unsigned long long key = keys[i];
-    int above = 0;
-    for (int j = 0; j < n; ++j) above += keys[j] > key;
-    if (above < k) out[above] = key;
-  }
+  if (w == 0) out[lane] = best;
   __syncthreads();
 }
 
@@ -288,18 +304,13 @@ __device__ __forceinline__ unsigned cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-// The other CTA's copy of a shared 64-bit word.
-__device__ __forceinline__ unsigned long long read_peer(const void* p, int rank) {
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// Writes the first CTA's copy of a shared 64-bit word.
+__device__ __forceinline__ void write_first(const void* p, unsigned long long v) {
   unsigned a;
-  unsigned long long v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-               : "=r"(a)
-               : "r"(static_cast<unsigned>(__cvta_generic_to_shared(p))), "r"(rank));
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
-  return v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(static_cast<unsigned>(__cvta_generic_to_shared(p))));
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 
 // One cluster of `parts` CTAs an item, each with an equal part of the row's
@@ -313,14 +324,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) logprobs_kernel(ScoreArgs a
   constexpr int E = Vec<T>::kLen;
   extern __shared__ unsigned long long s_keys[];        // [room]
   __shared__ unsigned s_seg[kTop ? kMaxSegs : 1];
-  __shared__ int s_chosen[32];
-  __shared__ unsigned long long s_top[32];
+  __shared__ unsigned long long s_best[kTop ? kMaxWarps : 1][32], s_top[32];
   __shared__ int s_count;
-  __shared__ unsigned s_tau;
   __shared__ Sums s_sums[kMaxWarps];
   __shared__ float s_m[kMaxWarps];
-  __shared__ double s_lse[2];
-  __shared__ unsigned long long s_mine[3];              // the CTA's largest logit and sums, for the cluster
+  __shared__ double s_lse[3];
+  // in the first CTA of a cluster: every CTA's largest logit, sums and alternatives
+  __shared__ unsigned long long s_peer[kMaxParts][3], s_peer_top[kTop ? kMaxParts : 1][32];
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, nt = blockDim.x, W = nt >> 5;
   const int parts = a.parts, part = parts > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int item = blockIdx.x / parts, V = a.V, k = a.top_k;
@@ -345,6 +355,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) logprobs_kernel(ScoreArgs a
     }
     return;
   }
+  if (parts > 1) cluster_arrive();  // the first CTA's shared memory is written only once it runs
   const Row<T> r(static_cast<const T*>(a.logits) + row * a.stride, V);
   const uint4* vecs = r.vecs();
   const float xt = part == 0 && tid == 0 ? to_float(r.x[tok]) : 0.f;
@@ -429,54 +440,47 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) logprobs_kernel(ScoreArgs a
   }
   if (tid == 0) s_count = 0;
   __syncthreads();
-  Sums all = s_sums[0];
-  m = s_m[0];
-  if (tid == 0) {
-    for (int j = 1; j < W; ++j) {
-      all = join(all, s_sums[j]);
-      m = fmaxf(m, s_m[j]);
+  Sums all{-INFINITY, 0.0, 0.0};
+  if (w == 0) {
+    m = -INFINITY;
+    if (lane < W) {
+      all = s_sums[lane];
+      m = s_m[lane];
     }
-    s_mine[0] = (static_cast<unsigned long long>(__float_as_uint(m)) << 32) | __float_as_uint(all.c);
-    s_mine[1] = __double_as_longlong(all.S);
-    s_mine[2] = __double_as_longlong(all.T);
+    all = join8(all);
+    m = order_value(__reduce_max_sync(0xffffffffu, order_of(m)));
   }
 
   if (kTop) {
-    // the segments to read again
+    // the segments to read again: below the k-th largest maximum is nothing to
+    // find; -inf is never a candidate
+    take_largest(segs, [&](int i) { return (static_cast<unsigned long long>(s_seg[i]) << 32) | (0xffffffffu - i); },
+                 s_best, s_top);
     const int chosen = min(k, segs);
-    for (int i = tid; i < segs; i += nt) {
-      const unsigned o = s_seg[i];
-      int above = 0;
-      for (int j = 0; j < segs; ++j) above += s_seg[j] > o || (s_seg[j] == o && j < i);
-      if (above < k) s_chosen[above] = i;
-      if (above == k - 1) s_tau = o;
-    }
-    __syncthreads();
-    // below tau there is nothing to find; -inf is never a candidate
-    const float tau = segs >= k ? order_value(s_tau) : -INFINITY;
+    const float tau = segs >= k ? order_value(static_cast<unsigned>(s_top[k - 1] >> 32)) : -INFINITY;
     const int units = chosen * a.group;                // rows of 32 vectors
     auto vec_of = [&](int unit) {                      // the lane's vector, -1: none
-      const int at = t0 * kAhead + s_chosen[unit / a.group] * a.group + unit % a.group;
+      const int at = t0 * kAhead + key_token(s_top[unit / a.group]) * a.group + unit % a.group;
       const int i = at * 32 + lane;
       return at < t1 * kAhead && i < r.nvec ? i : -1;
     };
-    auto offer = [&](float x, int v, unsigned long long above, int room) {
+    auto offer = [&](float x, int v, unsigned long long above) {
       if (!(x >= tau) || x == -INFINITY) return;
       const unsigned long long key = rank_key(x, v);
       if (key <= above) return;
       const int at = atomicAdd(&s_count, 1);
-      if (at < room) s_keys[at] = key;
+      if (at < a.room) s_keys[at] = key;
     };
-    auto offer_vec = [&](int i, const uint4& v, unsigned long long above, int room) {
+    auto offer_vec = [&](int i, const uint4& v, unsigned long long above) {
       if (i < 0 || !(Vec<T>::largest(v) >= tau)) return;
 #pragma unroll
       for (int j = 0; j < E / 2; ++j) {
         const F2 p = Vec<T>::pair(v, j);
-        offer(f2_lo(p), r.head + i * E + 2 * j, above, room);
-        offer(f2_hi(p), r.head + i * E + 2 * j + 1, above, room);
+        offer(f2_lo(p), r.head + i * E + 2 * j, above);
+        offer(f2_hi(p), r.head + i * E + 2 * j + 1, above);
       }
     };
-    if (end_at >= 0) offer(end_x, end_at, 0ull, a.room);
+    if (end_at >= 0) offer(end_x, end_at, 0ull);
     for (int u0 = w; u0 < units; u0 += 4 * W) {
       int i[4];
       uint4 v[4];
@@ -486,64 +490,75 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) logprobs_kernel(ScoreArgs a
         if (i[q] >= 0) v[q] = __ldg(vecs + i[q]);
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) offer_vec(i[q], v[q], 0ull, a.room);
+      for (int q = 0; q < 4; ++q) offer_vec(i[q], v[q], 0ull);
     }
     __syncthreads();
     const int found = s_count;
-    __syncthreads();
     if (found <= a.room) {
-      take_largest(s_keys, found, k, s_top, &s_count);
+      take_largest(found, [&](int i) { return s_keys[i]; }, s_best, s_top);
     } else {
       // more candidates than room (many equal or sorted logits): as many units
       // at a time as fit beside the best so far, which raise the bar
+      __shared__ unsigned long long s_so_far[32];
       const int step = (a.room - 32) / (32 * E);       // room is at least 32 + 32 E
       int have = 0;
       unsigned long long bar = 0ull;
       for (int u0 = 0; u0 < units; u0 += step) {
-        if (tid == 0) s_count = have;
         __syncthreads();
-        if (u0 == 0 && end_at >= 0) offer(end_x, end_at, 0ull, a.room);
+        if (tid == 0) s_count = have;
+        if (tid < have) s_keys[tid] = s_so_far[tid];
+        __syncthreads();
+        if (u0 == 0 && end_at >= 0) offer(end_x, end_at, 0ull);
         for (int u = u0 + w; u < min(units, u0 + step); u += W) {
           const int i = vec_of(u);
-          if (i >= 0) offer_vec(i, __ldg(vecs + i), bar, a.room);
+          if (i >= 0) offer_vec(i, __ldg(vecs + i), bar);
         }
         __syncthreads();
         const int n = s_count;
-        __syncthreads();
-        take_largest(s_keys, n, k, s_top, &s_count);
+        take_largest(n, [&](int i) { return s_keys[i]; }, s_best, s_so_far);
         have = min(n, k);
-        for (int i = tid; i < have; i += nt) s_keys[i] = s_top[i];
-        if (n >= k) bar = s_top[k - 1];
-        __syncthreads();
+        if (n >= k) bar = s_so_far[k - 1];
       }
+      __syncthreads();
+      if (tid < 32) s_top[tid] = tid < have ? s_so_far[tid] : 0ull;
+      __syncthreads();
     }
   }
 
   if (parts > 1) {
-    cluster_sync();
-    if (part == 0) {
-      if (tid == 0)
-        for (int p = 1; p < parts; ++p) {
-          const unsigned long long mc = read_peer(&s_mine[0], p);
-          m = fmaxf(m, __uint_as_float(static_cast<unsigned>(mc >> 32)));
-          all = join(all, Sums{__uint_as_float(static_cast<unsigned>(mc)), __longlong_as_double(read_peer(&s_mine[1], p)),
-                               __longlong_as_double(read_peer(&s_mine[2], p))});
-        }
-      if (kTop) {
-        if (tid == 0) s_count = 0;
-        __syncthreads();
-        for (int i = tid; i < parts * k; i += nt) {
-          const unsigned long long key = i < k ? s_top[i] : read_peer(&s_top[i % k], i / k);
-          if (key != 0ull) s_keys[atomicAdd(&s_count, 1)] = key;    // room >= 8 * 32
-        }
-        __syncthreads();
-        const int n = s_count;
-        __syncthreads();
-        take_largest(s_keys, n, k, s_top, &s_count);
+    cluster_wait();
+    if (w == 0) {
+      if (lane == 0) {
+        write_first(&s_peer[part][0],
+                    (static_cast<unsigned long long>(__float_as_uint(m)) << 32) | __float_as_uint(all.c));
+        write_first(&s_peer[part][1], __double_as_longlong(all.S));
+        write_first(&s_peer[part][2], __double_as_longlong(all.T));
       }
+      if (kTop) write_first(&s_peer_top[part][lane], lane < k ? s_top[lane] : 0ull);
     }
-    cluster_sync();
+    cluster_arrive();
+    cluster_wait();
     if (part != 0) return;
+    if (w == 0) {
+      m = -INFINITY;
+      all = Sums{-INFINITY, 0.0, 0.0};
+      if (lane < parts) {
+        const unsigned long long mc = s_peer[lane][0];
+        m = __uint_as_float(static_cast<unsigned>(mc >> 32));
+        all = Sums{__uint_as_float(static_cast<unsigned>(mc)), __longlong_as_double(s_peer[lane][1]),
+                   __longlong_as_double(s_peer[lane][2])};
+      }
+      all = join8(all);
+      m = order_value(__reduce_max_sync(0xffffffffu, order_of(m)));
+    }
+    if (kTop)     // sorted lists: merged in pairs
+      for (int n = parts / 2; n > 0; n /= 2) {
+        for (int p = w; p < n; p += W) {
+          const unsigned long long best = merge32(s_peer_top[p][lane], s_peer_top[p + n][lane], lane);
+          (n == 1 ? s_top : s_peer_top[p])[lane] = best;
+        }
+        __syncthreads();
+      }
   }
   const bool bad = !(all.S < 1e300);   // a NaN or +inf in the row
   if (tid == 0) {
@@ -559,23 +574,21 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) logprobs_kernel(ScoreArgs a
     if (a.stats != nullptr)
       reinterpret_cast<float2*>(a.stats)[item] =
           bad ? make_float2(NAN, NAN) : make_float2(m, static_cast<float>(all.S * exp2(off)));
-    if (kTop) {
-      s_lse[0] = top;
-      s_lse[1] = lnS;
-      s_count = bad;
-    }
+    s_lse[0] = top;
+    s_lse[1] = lnS;
+    s_lse[2] = bad ? 1.0 : 0.0;
   }
-  if (kTop) {
-    __syncthreads();
+  if (kTop && w == 0) {
+    __syncwarp();
     const double top = s_lse[0], lnS = s_lse[1];
-    for (int i = tid; i < k; i += nt) {
-      const unsigned long long key = s_top[i];
-      const long long o = static_cast<long long>(item) * k + i;
-      const float none = s_count ? NAN : -INFINITY;
+    const bool nan = s_lse[2] != 0.0;
+    if (lane < k) {
+      const unsigned long long key = s_top[lane];
+      const long long o = static_cast<long long>(item) * k + lane;
       a.top_tokens[o] = key != 0ull ? key_token(key) : -1;
-      a.top_logprobs[o] = key == 0ull || s_count
-                              ? none
-                              : static_cast<float>(order_value(static_cast<unsigned>(key >> 32)) - top - lnS);
+      a.top_logprobs[o] = nan ? NAN
+                          : key == 0ull ? -INFINITY
+                                        : static_cast<float>(order_value(static_cast<unsigned>(key >> 32)) - top - lnS);
     }
   }
 }
@@ -664,7 +677,7 @@ cudaError_t launch_logprobs(ScoreArgs a, int items, cudaStream_t s) {
   // few rows: a row is shared by up to 8 CTAs (a portable cluster), while that
   // leaves each CTA eight tiles or more
   int parts = 1;
-  while (parts < 8 && static_cast<long long>(items) * parts < 4 * kSms && tiles / (2 * parts) >= 8) parts *= 2;
+  while (parts < kMaxParts && static_cast<long long>(items) * parts < 4 * kSms && tiles / (2 * parts) >= 8) parts *= 2;
   const int most = (tiles + parts - 1) / parts;
   a.parts = parts;
   // segments of one row of 32 vectors while shared memory holds so many, else
