@@ -35,7 +35,9 @@ struct ScoreArgs {
   int32_t* top_tokens;
   float* top_logprobs;
   unsigned* err;
+  int items;
   int parts;   // CTAs of a cluster, each with an equal part of the row
+  int gather;  // the items left out come last in the grid
   int group;   // rows of 32 vectors of a segment (alternatives): 1, or a multiple of kAhead
   int room;    // candidates that shared memory holds
 };
@@ -151,6 +153,7 @@ struct Row {
 constexpr int kAhead = 4;                 // vectors of a lane in flight
 constexpr int kTile = 32 * kAhead;        // vectors of a tile: one warp, one step
 constexpr int kMaxWarps = 8;
+constexpr int kGather = 16384;            // items up to which the items left out come last
 constexpr int kMaxParts = 8;              // CTAs of a row (the portable cluster size)
 constexpr int kMaxSegs = 256;             // segments of a CTA's part
 constexpr float kSlack = 4.f;             // how far logits may exceed the sums' c before it is raised
@@ -313,6 +316,41 @@ __device__ __forceinline__ void write_first(const void* p, unsigned long long v)
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 
+// The item that comes `index`-th when the items left out (token -1) come last:
+// otherwise a batch's short requests leave some SMs with four rows to read
+// and others with none. Each CTA counts all tokens by itself; the order is by
+// the thread that looks at an item, the same in every CTA.
+__device__ int gathered_item(const int32_t* tokens, int items, int index, int* s_before, int* s_item) {
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, nt = blockDim.x;
+  int used = 0, seen = 0;
+  for (int i = tid; i < items; i += nt) {
+    used += __ldg(tokens + i) != -1;
+    ++seen;
+  }
+  int inc = used;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) s_before[w] = inc;
+  __syncthreads();
+  int before = inc - used, total = 0;
+  for (int j = 0; j < (nt >> 5); ++j) {
+    if (j < w) before += s_before[j];
+    total += s_before[j];
+  }
+  // items of the threads in front: items / nt each, and one more of the first
+  const int skipped_before = tid * (items / nt) + min(tid, items % nt) - before;
+  const bool out = index >= total;
+  int rank = out ? index - total - skipped_before : index - before;
+  if (rank >= 0 && rank < (out ? seen - used : used))
+    for (int i = tid; i < items; i += nt)
+      if ((__ldg(tokens + i) != -1) != out && rank-- == 0) *s_item = i;
+  __syncthreads();
+  return *s_item;
+}
+
 // One cluster of `parts` CTAs an item, each with an equal part of the row's
 // tiles. Alternatives: the top_k elements lie in the top_k segments with the
 // largest maxima (equal ones: the first), because each segment in front of
@@ -333,7 +371,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) logprobs_kernel(ScoreArgs a
   __shared__ unsigned long long s_peer[kMaxParts][3], s_peer_top[kTop ? kMaxParts : 1][32];
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, nt = blockDim.x, W = nt >> 5;
   const int parts = a.parts, part = parts > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int item = blockIdx.x / parts, V = a.V, k = a.top_k;
+  const int V = a.V, k = a.top_k;
+  __shared__ int s_before[kMaxWarps + 1], s_item;
+  int item = blockIdx.x / parts;
+  if (a.gather) item = gathered_item(a.tokens, a.items, item, s_before, &s_item);
   const int b = item / a.C;
   const int tok = a.tokens[item];
   bool skip = tok == -1;
@@ -674,17 +715,29 @@ template <typename T>
 cudaError_t launch_logprobs(ScoreArgs a, int items, cudaStream_t s) {
   constexpr int E = Vec<T>::kLen;
   const int tiles = std::max(1, (a.V / E + kTile - 1) / kTile);
-  // few rows: a row is shared by up to 8 CTAs (a portable cluster), while that
-  // leaves each CTA eight tiles or more
+  // rows to read, as far as can be told here: a round's emitted tokens fill
+  // about half of its items or less
+  const long long rows = a.C > 1 ? (items + 1) / 2 : items;
+  // few rows: a row is shared by the CTAs of a cluster, while that leaves each
+  // eight tiles or more. Two CTAs up to four an SM; four and eight, whose
+  // placing leaves SMs unevenly filled, up to two an SM (rows of 151,936 fp32:
+  // 74 by 2 CTAs 17.6 us, by 4 13.0, by 8 15.9; 148 by 1 28.5, by 2 19.9, by
+  // 4 25.1; 296 by 1 34.5, by 2 30.8; 366 by 1 38.9, by 2 45.5)
   int parts = 1;
-  while (parts < kMaxParts && static_cast<long long>(items) * parts < 4 * kSms && tiles / (2 * parts) >= 8) parts *= 2;
+  while (parts < kMaxParts && rows * 2 * parts <= (parts == 1 ? 4 * kSms : 2 * kSms) && tiles / (2 * parts) >= 8)
+    parts *= 2;
   const int most = (tiles + parts - 1) / parts;
+  a.items = items;
   a.parts = parts;
+  a.gather = a.C > 1 && items > kSms / 2 && items <= kGather;
   // segments of one row of 32 vectors while shared memory holds so many, else
   // of whole tiles: fewer maxima to note (one a tile), more to read again
   a.group = most * kAhead <= kMaxSegs ? 1 : (most + kMaxSegs - 1) / kMaxSegs * kAhead;
+  // many short rows: twice as many CTAs of four warps (4,000 rows of 32,000
+  // bf16 with 5 alternatives 78.8 -> 69.3 us, 1,000 of 5,000 fp32 7.8 -> 5.8;
+  // 366 of 151,936 fp32 39.5 -> 56)
+  const int warps = std::min(most, rows > 4 * kSms && most <= 64 ? kMaxWarps / 2 : kMaxWarps);
   a.room = 32 + std::max(32 * E, std::min(kRoom, most * kTile * E));
-  const int warps = std::min(most, kMaxWarps);
   const bool top = a.top_k > 0;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(items) * parts);
@@ -733,7 +786,7 @@ dspark_status dspark_logprobs(const void* logits, dspark_dtype dtype, int64_t n_
   if (top_k > 0 && (!given(top_tokens) || !given(top_logprobs))) return DSPARK_ERR_INVALID_ARG;
   if (ws_bytes < kScratchOffset) return DSPARK_ERR_INVALID_ARG;
   ScoreArgs a{logits, n_rows, row_stride, row_start, tokens, C, V, top_k, logprob, entropy, stats, top_tokens,
-              top_logprobs, reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + kErrOffset), 1, 1, 0};
+              top_logprobs, reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + kErrOffset), 0, 1, 0, 1, 0};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == DSPARK_F32 ? launch_logprobs<float>(a, B * C, s) : launch_logprobs<uint16_t>(a, B * C, s);
   return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
