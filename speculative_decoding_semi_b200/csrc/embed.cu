@@ -154,21 +154,23 @@ cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t s) {
 
 // -------------------------------------------------------------- gradient
 //
-// dtable[v] = scale * sum of dout's rows whose token is v. Two kernels:
+// dtable[v] = scale * sum of dout's rows whose token is v. Three kernels, each started
+// while the one before it runs out:
 //
 // sort_kernel: CTA g owns table rows [g R, (g+1) R). It reads all n tokens,
 //   counts those below its rows (its offset in the sorted order, so the CTAs
-//   need not talk to each other) and counting-sorts its own, stably: each of
-//   16 warps takes a contiguous piece of the tokens, keeps its matches in
-//   order, counts them per row, and places them after the earlier warps'.
-//   It then zeroes its rows that no token points at.
-// sum_kernel: the sorted items in equal pieces, whatever the lengths of the
-//   runs of equal tokens, so that a frequent token is summed by many CTAs. A
-//   run inside a piece is written at once; the parts of a run that crosses
-//   pieces go to scratch, and the CTA that delivers the last part (a counter)
-//   adds them in order. Which CTA that is does not change the order.
+//   need not talk to each other) and counting-sorts its own, stably: each
+//   warp takes a contiguous piece of the tokens, keeps its matches in order,
+//   counts them per row, and places them after the earlier warps'. It then
+//   zeroes its rows that no token points at.
+// sum_kernel: the sorted items in windows of equal length, one a warp. A short
+//   run of equal tokens is summed by the warp in whose window it starts. A
+//   longer one is summed by all whose windows it touches, so that a frequent
+//   token does not hold up one CTA; their parts go to scratch.
+// join_kernel: adds the parts of each long run in order.
 //
-// Few items with accumulate: direct_kernel, one CTA an item, no sorting.
+// Few items: direct_kernel, one CTA an item, no sorting; without accumulate it
+// runs beside zero_kernel and waits for it before it writes.
 
 struct GradArgs {
   const void* dout;
@@ -178,18 +180,19 @@ struct GradArgs {
   int accumulate;
   void* dtable;
   unsigned* err;
-  int R, slabs, pieces;   // table rows of an owner; 128-column slabs; pieces of the sorted items
+  int R, slabs, pieces;   // table rows of an owner; slabs of a row; pieces (a CTA's windows) of the sorted items
+  int keep;               // matches that a warp of the sort keeps in shared memory; more are found again
   int* n_sorted;          // items with a token
-  unsigned* arrived;      // [pieces][slabs] parts of the run that starts in a piece and leaves it
   int4* sorted;           // [n] item, token, and the run [begin, end) it is in
-  float* parts;           // [pieces][2][slabs * 128]: of the run that comes in, of the run that leaves
+  float* parts;           // [windows][2][slabs][32 lanes]: of the long run that comes in, of the one that starts
 };
 
 constexpr int kSortWarps = 16, kSortThreads = kSortWarps * 32;
 constexpr int kMaxR = 2048;     // rows of an owner (11 bits beside 20 of an item's place in a warp's piece)
-constexpr int kKeep = 512;      // matches that a warp keeps in shared memory; more are found again
-constexpr int kSumWarps = 8, kSumThreads = kSumWarps * 32;
-constexpr int kSlab = 128;      // columns of a warp's quad: four a lane
+constexpr int kWindow = 16;     // sorted items of a warp
+constexpr int kShort = 16;      // a run up to this length belongs to one warp (kWindow + kShort <= 32)
+constexpr int kAhead = 8;       // rows of a warp in flight
+constexpr int kSumWarps = 8, kSumThreads = kSumWarps * 32, kPiece = kSumWarps * kWindow;
 constexpr int kDirectItems = 1024;
 constexpr int kDirectWarps = 8, kDirectThreads = kDirectWarps * 32;
 
@@ -203,29 +206,56 @@ __device__ __forceinline__ void zero_row(TO* d, int r, int lane) {
   }
 }
 
+// 16 warps sort. With accumulate off 16 more zero the rows meanwhile, blindly
+// until the counts are known (what they zero of rows with tokens sum_kernel
+// writes over), then only those without a token; the sorting warps join them.
 template <typename TO>
-__global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(GradArgs a) {
+__global__ void __launch_bounds__(2 * kSortThreads, 1) sort_kernel(GradArgs a) {
   extern __shared__ unsigned smem[];
-  unsigned* hist = smem;                                   // [16][R] counts, then places
-  unsigned* total = hist + kSortWarps * a.R;               // [R] tokens of a row
-  unsigned* kept = total + a.R;                            // [16][kKeep]
-  __shared__ unsigned s_below, s_red[kSortWarps];
+  constexpr int W = kSortWarps, nt = kSortThreads;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, R = a.R, n = a.n;
+  unsigned* hist = smem;                                   // [W][R] counts, then places
+  unsigned* total = hist + W * R;                          // [R] tokens of a row
+  unsigned* begin = total + R;                             // [R] and where they start in the sorted order
+  unsigned* mine = begin + R + w * a.keep;                 // [W][keep]
+  __shared__ unsigned s_below, s_red[W];
+  __shared__ int s_rows;
+  __shared__ volatile int s_counted;
   const int v0 = blockIdx.x * R, rows = min(R, a.V - v0);
-  const unsigned lt = (1u << lane) - 1u;
-  for (int k = tid; k < kSortWarps * R; k += kSortThreads) hist[k] = 0;
-  if (tid == 0) s_below = 0;
-  for (int k = blockIdx.x * kSortThreads + tid; k < a.pieces * a.slabs; k += gridDim.x * kSortThreads) a.arrived[k] = 0;
+  auto fill = [&]() {          // by whole warps, four rows at a time
+    TO* d = static_cast<TO*>(a.dtable) + static_cast<long long>(v0) * a.r;
+    while (true) {
+      int k = 0;
+      if (lane == 0) k = atomicAdd(&s_rows, 4);
+      k = __shfl_sync(0xffffffffu, k, 0);
+      if (k >= rows) return;
+      const bool counted = s_counted != 0;
+      __threadfence_block();
+      for (int j = k; j < min(rows, k + 4); ++j)
+        if (!counted || total[j] == 0u) zero_row(d + static_cast<long long>(j) * a.r, a.r, lane);
+    }
+  };
+  if (tid == 0) {
+    s_rows = 0;
+    s_counted = 0;
+    s_below = 0;
+  }
   __syncthreads();
+  if (w >= W) {
+    fill();
+    return;
+  }
+  using Sorters = NamedSync<1, kSortThreads>;
+  const unsigned lt = (1u << lane) - 1u;
+  for (int k = tid; k < W * R; k += nt) hist[k] = 0;
+  Sorters::sync();
 
   // each warp's matches, in order: four neighbouring tokens a lane
-  const int len = ceil_div(ceil_div(n, kSortWarps), 128) * 128;
+  const int len = ceil_div(ceil_div(n, W), 128) * 128;
   const int lo = min(n, w * len), hi = min(n, lo + len);
-  unsigned* mine = kept + w * kKeep;
   unsigned* count = hist + w * R;
   int found = 0;
   unsigned below = 0;
-  constexpr int kAhead = 8;
   for (int i0 = lo; i0 < hi; i0 += 128 * kAhead) {
     int4 q[kAhead];
 #pragma unroll
@@ -269,7 +299,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(GradArgs a) {
         if (!hit[c]) continue;
         const unsigned off = static_cast<unsigned>(t[c] - v0);
         atomicAdd(count + off, 1u);
-        if (at < kKeep) mine[at] = (static_cast<unsigned>(i + c - lo) << 11) | off;
+        if (at < a.keep) mine[at] = (static_cast<unsigned>(i + c - lo) << 11) | off;
         ++at;
       }
     }
@@ -277,15 +307,15 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(GradArgs a) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
   if (lane == 0 && below != 0u) atomicAdd(&s_below, below);
-  __syncthreads();
+  Sorters::sync();
 
   // places: rows in order, within a row the warps in order
-  const int per = ceil_div(rows, kSortThreads), r0 = min(rows, tid * per), r1 = min(rows, r0 + per);
+  const int per = ceil_div(rows, nt), r0 = min(rows, tid * per), r1 = min(rows, r0 + per);
   unsigned sum = 0;
   for (int k = r0; k < r1; ++k) {
     unsigned c = 0;
-#pragma unroll
-    for (int j = 0; j < kSortWarps; ++j) {
+#pragma unroll 8
+    for (int j = 0; j < W; ++j) {
       const unsigned x = hist[j * R + k];
       hist[j * R + k] = c;
       c += x;
@@ -300,229 +330,355 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(GradArgs a) {
     if (lane >= o) inc += x;
   }
   if (lane == 31) s_red[w] = inc;
-  __syncthreads();
+  Sorters::sync();
+  if (tid == 0) {                    // behind the barrier: every total is there
+    __threadfence_block();
+    s_counted = 1;
+  }
   unsigned place = s_below + inc - sum;
   for (int j = 0; j < w; ++j) place += s_red[j];
   for (int k = r0; k < r1; ++k) {
-#pragma unroll
-    for (int j = 0; j < kSortWarps; ++j) hist[j * R + k] += place;
-    place += total[k];
+    begin[k] = place;
+    if (total[k] != 0u) {
+#pragma unroll 8
+      for (int j = 0; j < W; ++j) hist[j * R + k] += place;
+      place += total[k];
+    }
   }
-  if (blockIdx.x == gridDim.x - 1 && tid == kSortThreads - 1) *a.n_sorted = static_cast<int>(place);
-  __syncthreads();
+  if (blockIdx.x == gridDim.x - 1 && tid == nt - 1) *a.n_sorted = static_cast<int>(place);
+  Sorters::sync();
 
   auto put = [&](bool hit, unsigned off, int item) {   // by the whole warp
     const unsigned peers = __match_any_sync(0xffffffffu, hit ? off : 0xffffffffu);
     if (hit) {
-      const int at = static_cast<int>(count[off]) + __popc(peers & lt);
-      // the run: warp 0's first place to the last warp's end
-      a.sorted[at] = make_int4(item, v0 + static_cast<int>(off), 0, 0);
+      const int first = static_cast<int>(begin[off]);
+      a.sorted[count[off] + __popc(peers & lt)] =
+          make_int4(item, v0 + static_cast<int>(off), first, first + static_cast<int>(total[off]));
     }
     __syncwarp();
     if (hit && (peers & lt) == 0u) count[off] += __popc(peers);
     __syncwarp();
   };
-  if (found <= kKeep) {
+  if (found <= a.keep) {
     for (int k0 = 0; k0 < found; k0 += 32) {
       const bool hit = k0 + lane < found;
       const unsigned e = hit ? mine[k0 + lane] : 0u;
       put(hit, e & 2047u, lo + static_cast<int>(e >> 11));
     }
   } else {
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-      const int i = i0 + lane, t = i < hi ? __ldg(a.tokens + i) : -1;
-      const unsigned off = static_cast<unsigned>(t - v0);
-      const bool hit = t >= 0 && off < static_cast<unsigned>(rows);
-      if (__any_sync(0xffffffffu, hit)) put(hit, off, i);
+    for (int i0 = lo; i0 < hi; i0 += 32 * kAhead) {
+      int t[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * 32 + lane;
+        t[u] = i < hi ? __ldg(a.tokens + i) : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const bool hit = t[u] >= v0 && t[u] < v0 + rows;
+        if (__any_sync(0xffffffffu, hit)) put(hit, static_cast<unsigned>(t[u] - v0), i0 + u * 32 + lane);
+      }
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __syncthreads();
-  // after the placement the last warp's place is each run's end
-  const unsigned* ends = hist + (kSortWarps - 1) * R;
-  for (int k = w; k < rows; k += kSortWarps) {
-    const int c = static_cast<int>(total[k]), end = static_cast<int>(ends[k]);
-    for (int j = lane; j < c; j += 32) {
-      int4* s = a.sorted + (end - c + j);
-      reinterpret_cast<int2*>(s)[1] = make_int2(end - c, end);
-    }
-    if (c == 0 && !a.accumulate) zero_row(static_cast<TO*>(a.dtable) + static_cast<long long>(v0 + k) * a.r, a.r, lane);
-  }
+  if (!a.accumulate) fill();
 }
 
-// Four columns of a row: neighbours (r a multiple of 4), or 32 apart. A slab
-// of a warp is kQuads times 128 columns.
-template <typename T, bool kVec>
-__device__ __forceinline__ float4 load_quad(const T* p, int lane, int cols) {
-  float4 v = make_float4(0, 0, 0, 0);
-  if constexpr (!kVec) {
-    if (lane < cols) v.x = to_float(p[lane]);
-    if (lane + 32 < cols) v.y = to_float(p[lane + 32]);
-    if (lane + 64 < cols) v.z = to_float(p[lane + 64]);
-    if (lane + 96 < cols) v.w = to_float(p[lane + 96]);
-  } else if (lane * 4 < cols) {
-    if constexpr (sizeof(T) == 4) {
-      v = __ldcs(reinterpret_cast<const float4*>(p) + lane);
-    } else {
-      const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p) + lane);
-      v = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                      __uint_as_float(u.y & 0xffff0000u));
+// A lane's columns of a row of TI, 16 bytes: neighbours (kVec: the rows are
+// aligned to that), or 32 apart. A slab is a warp's columns.
+template <typename TI>
+constexpr int kLane = 16 / static_cast<int>(sizeof(TI));
+template <typename TI>
+constexpr int kSlab = 32 * kLane<TI>;
+
+template <typename TI, bool kVec>
+__device__ __forceinline__ uint4 load_lane(const TI* p, int lane, int cols) {
+  constexpr int E = kLane<TI>;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if constexpr (kVec) {
+    if (lane * E < cols) v = __ldcs(reinterpret_cast<const uint4*>(p) + lane);
+  } else {
+    unsigned x[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      x[j] = 0u;
+      if (lane + 32 * j < cols) {
+        if constexpr (E == 4)
+          x[j] = __float_as_uint(p[lane + 32 * j]);
+        else
+          x[j] = p[lane + 32 * j];
+      }
     }
+    if constexpr (E == 4)
+      v = make_uint4(x[0], x[1], x[2], x[3]);
+    else
+      v = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
   }
   return v;
 }
-template <typename T, bool kVec>
-__device__ __forceinline__ void save_quad(T* p, int lane, int cols, float4 v) {
-  if constexpr (!kVec) {
-    if (lane < cols) store(p + lane, v.x);
-    if (lane + 32 < cols) store(p + lane + 32, v.y);
-    if (lane + 64 < cols) store(p + lane + 64, v.z);
-    if (lane + 96 < cols) store(p + lane + 96, v.w);
-  } else if (lane * 4 < cols) {
-    if constexpr (sizeof(T) == 4)
-      reinterpret_cast<float4*>(p)[lane] = v;
-    else
-      reinterpret_cast<uint2*>(p)[lane] = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+
+template <int E>
+__device__ __forceinline__ void add_lane(float (&s)[E], const uint4& v) {
+  const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (E == 4) {
+      s[j] += __uint_as_float(w[j]);
+    } else {
+      s[2 * j] += __uint_as_float(w[j] << 16);
+      s[2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+    }
   }
 }
 
-__device__ __forceinline__ float4 plus(float4 a, float4 b) {
-  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+template <int E>
+__device__ __forceinline__ void clear(float (&s)[E]) {
+#pragma unroll
+  for (int j = 0; j < E; ++j) s[j] = 0.f;
 }
 
-// dtable[token, quad] (+)= scale * sum; `col` the quad's first column
-template <typename TO, bool kVec>
-__device__ __forceinline__ void finish(const GradArgs& a, int token, int col, int lane, float4 s) {
+template <typename TO, bool kVec, int E>
+__device__ __forceinline__ void save_lane(TO* d, int lane, int cols, const float (&v)[E]) {
+  if constexpr (kVec) {
+    if (lane * E < cols) save_cols<E>(d + lane * E, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (lane + 32 * j < cols) store(d + lane + 32 * j, v[j]);
+  }
+}
+
+// dtable[token, a lane's columns from col on] (+)= scale * s
+template <typename TO, bool kVec, int E>
+__device__ __forceinline__ void finish(const GradArgs& a, int token, int col, int lane, const float (&s)[E]) {
   TO* d = static_cast<TO*>(a.dtable) + static_cast<long long>(token) * a.r + col;
-  s = make_float4(s.x * a.scale, s.y * a.scale, s.z * a.scale, s.w * a.scale);
-  if (a.accumulate) s = plus(s, load_quad<TO, kVec>(d, lane, a.r - col));
-  save_quad<TO, kVec>(d, lane, a.r - col, s);
+  const int cols = a.r - col;
+  float v[E];
+#pragma unroll
+  for (int j = 0; j < E; ++j) v[j] = s[j] * a.scale;
+  if (a.accumulate) {
+    float old[E];
+    clear(old);
+    if constexpr (kVec) {
+      if (lane * E < cols) load_cols<E>(d + lane * E, old);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (lane + 32 * j < cols) old[j] = to_float(d[lane + 32 * j]);
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j) v[j] += old[j];
+  }
+  save_lane<TO, kVec, E>(d, lane, cols, v);
 }
 
-// A piece is kSumWarps * P sorted items, P a warp, on one slab.
-template <typename TI, typename TO, bool kVec, int kQuads, int P>
-__global__ void __launch_bounds__(kSumThreads, 4) sum_kernel(GradArgs a) {
-  constexpr int kPiece = kSumWarps * P;
-  constexpr int kRowsAhead = 8 / kQuads;
-  __shared__ float4 s_part[kSumWarps][2][kQuads][32];
-  __shared__ int4 s_run[kSumWarps][2];   // token, begin, end of each part; token -1: none
+// A lane's columns (16 bytes of TI) of a row to its place in shared memory,
+// without waiting; where the rows are not aligned, by way of registers.
+template <typename T, bool kVec, int E>
+__device__ __forceinline__ void fetch_lane(T* to, const T* p, int lane, int cols) {
+  constexpr int kBytes = E * static_cast<int>(sizeof(T)), kStep = kBytes < 16 ? kBytes : 16;
+  if constexpr (kVec) {
+    if (lane * E < cols) {
+      const unsigned at = static_cast<unsigned>(__cvta_generic_to_shared(to));
+#pragma unroll
+      for (int j = 0; j < kBytes; j += kStep)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at + j),
+                     "l"(reinterpret_cast<const char*>(p + lane * E) + j), "n"(kStep)
+                     : "memory");
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (lane + 32 * j < cols) to[j] = p[lane + 32 * j];
+  }
+}
+
+template <typename TI, typename TO, bool kAdd>
+struct SumShared {
+  static constexpr int E = kLane<TI>;
+  struct __align__(16) In {
+    TI v[E];
+  };
+  struct __align__(16) Old {
+    TO v[E];
+  };
+  In rows[kSumWarps][kAhead][32];
+  Old old[kAdd ? kSumWarps : 1][kAdd ? kAhead : 1][32];
+};
+
+// A lane's place in the scratch for window g's part of a long run: the run
+// that comes in (k = 0), or starts there (1).
+template <int E>
+__device__ __forceinline__ float4* part_of(const GradArgs& a, int g, int k, int slab, int lane) {
+  return reinterpret_cast<float4*>(a.parts) + (((2ll * g + k) * a.slabs + slab) * 32 + lane) * (E / 4);
+}
+
+// A warp is on its own: one window, one slab.
+template <typename TI, typename TO, bool kVec, bool kAdd>
+__global__ void __launch_bounds__(kSumThreads, kAdd ? 2 : 4) sum_kernel(GradArgs a) {
+  constexpr int E = kLane<TI>;
+  extern __shared__ __align__(16) unsigned char sum_smem[];
+  SumShared<TI, TO, kAdd>& sh = *reinterpret_cast<SumShared<TI, TO, kAdd>*>(sum_smem);
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int piece = blockIdx.x / a.slabs, slab = blockIdx.x - piece * a.slabs;
-  const int p0 = piece * kPiece, lo = p0 + w * P, col0 = slab * kQuads * kSlab;
+  const int window = piece * kSumWarps + w, lo = window * kWindow, pos = lo + lane;
+  const int col = slab * kSlab<TI>, cols = a.r - col;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // what lies behind the last sorted item is read but not used
-  int4 it = make_int4(0, -1, 0, 0);
-  if (lane < P && lo + lane < a.n) it = __ldcg(a.sorted + lo + lane);
-  const int N = __ldcg(a.n_sorted);
-  if (p0 >= N) return;
-  const int hi = min(N, lo + P);
-  const TI* dout = static_cast<const TI*>(a.dout) + col0;
-  if (lane < 2) s_run[w][lane].x = -1;
-  const unsigned ends = __ballot_sync(0xffffffffu, lo + lane < hi && (lo + lane == it.w - 1 || lo + lane == hi - 1));
-  float4 sum[kQuads];
+  int4 it = make_int4(0, 0, 0, 0);
+  if (pos < a.n) it = __ldcg(a.sorted + pos);
+  const int N = __ldcg(a.n_sorted), hi = min(N, lo + kWindow);
+  if (lo >= N) return;
+  const bool is_short = it.w - it.z <= kShort;
+  const bool mine = pos < N && (is_short ? it.z >= lo && it.z < hi : pos < hi);
+  unsigned left = __ballot_sync(0xffffffffu, mine);
+  const unsigned ends = __ballot_sync(0xffffffffu, mine && (pos == it.w - 1 || (!is_short && pos == hi - 1)));
+  const unsigned shorts = __ballot_sync(0xffffffffu, is_short);
+  const TI* dout = static_cast<const TI*>(a.dout) + col;
+  TO* dtable = static_cast<TO*>(a.dtable) + col;
+  float sum[E];
+  clear(sum);
+  while (left != 0u) {
+    unsigned todo = left;
 #pragma unroll
-  for (int q = 0; q < kQuads; ++q) sum[q] = make_float4(0, 0, 0, 0);
+    for (int u = 0; u < kAhead; ++u) {
+      const int at = __ffs(todo) - 1;
+      const int item = __shfl_sync(0xffffffffu, it.x, at & 31), token = __shfl_sync(0xffffffffu, it.y, at & 31);
+      if (todo != 0u) {
+        fetch_lane<TI, kVec, E>(sh.rows[w][u][lane].v, dout + static_cast<long long>(item) * a.r, lane, cols);
+        if (kAdd && ((ends & shorts) >> at & 1u) != 0u)      // what the run's sum is added to
+          fetch_lane<TO, kVec, E>(sh.old[kAdd ? w : 0][kAdd ? u : 0][lane].v,
+                                  dtable + static_cast<long long>(token) * a.r, lane, cols);
+      }
+      todo &= todo - 1;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
-  for (int j0 = 0; lo + j0 < hi && j0 < P; j0 += kRowsAhead) {
-    float4 x[kRowsAhead][kQuads];
+    for (int u = 0; u < kAhead && left != 0u; ++u) {
+      const int at = __ffs(left) - 1;
+      left &= left - 1;
 #pragma unroll
-    for (int u = 0; u < kRowsAhead; ++u) {
-      const int item = __shfl_sync(0xffffffffu, it.x, j0 + u);
+      for (int j = 0; j < E; ++j) sum[j] += to_float(sh.rows[w][u][lane].v[j]);
+      if ((ends >> at & 1u) == 0u) continue;
+      if ((shorts >> at & 1u) != 0u) {
+        const int token = __shfl_sync(0xffffffffu, it.y, at);
 #pragma unroll
-      for (int q = 0; q < kQuads; ++q)
-        x[u][q] = lo + j0 + u < hi ? load_quad<TI, kVec>(dout + static_cast<long long>(item) * a.r + q * kSlab, lane,
-                                                         a.r - col0 - q * kSlab)
-                                   : make_float4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int u = 0; u < kRowsAhead; ++u) {
-#pragma unroll
-      for (int q = 0; q < kQuads; ++q) sum[q] = plus(sum[q], x[u][q]);
-      if ((ends >> (j0 + u)) & 1u) {      // the run, or this warp's part of it, ends here
-        const int token = __shfl_sync(0xffffffffu, it.y, j0 + u);
-        const int begin = __shfl_sync(0xffffffffu, it.z, j0 + u), end = __shfl_sync(0xffffffffu, it.w, j0 + u);
-        const int k = begin < lo ? 0 : 1;       // came in, or leaves
-        const bool whole = begin >= lo && end <= hi;
-        if (!whole && lane == 0) s_run[w][k] = make_int4(token, begin, end, 0);
-#pragma unroll
-        for (int q = 0; q < kQuads; ++q) {
-          if (whole)
-            finish<TO, kVec>(a, token, col0 + q * kSlab, lane, sum[q]);
-          else
-            s_part[w][k][q][lane] = sum[q];
-          sum[q] = make_float4(0, 0, 0, 0);
+        for (int j = 0; j < E; ++j) {
+          sum[j] *= a.scale;
+          if (kAdd) sum[j] += to_float(sh.old[kAdd ? w : 0][kAdd ? u : 0][lane].v[j]);
         }
+        save_lane<TO, kVec, E>(dtable + static_cast<long long>(token) * a.r, lane, cols, sum);
+      } else {
+        // a long run's part: it came in, or starts here (and leaves: it is longer than a window)
+        float4* part = part_of<E>(a, window, __shfl_sync(0xffffffffu, it.z, at) < lo ? 0 : 1, slab, lane);
+#pragma unroll
+        for (int j = 0; j < E / 4; ++j)
+          part[j] = make_float4(sum[4 * j], sum[4 * j + 1], sum[4 * j + 2], sum[4 * j + 3]);
       }
+      clear(sum);
     }
   }
+}
+
+// Adds parts [lo, hi) of the long run whose parts start at window `first`.
+template <int E>
+__device__ __forceinline__ void add_parts(const GradArgs& a, int first, int lo, int hi, int slab, int lane,
+                                          float (&sum)[E]) {
+  constexpr int kParts = 32 / E;
+  for (int g = lo; g < hi; g += kParts) {
+    float4 x[kParts][E / 4];
+#pragma unroll
+    for (int u = 0; u < kParts; ++u)
+#pragma unroll
+      for (int j = 0; j < E / 4; ++j)
+        x[u][j] = g + u < hi ? __ldcg(part_of<E>(a, first + g + u, g + u == 0 ? 1 : 0, slab, lane) + j)
+                             : make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < kParts; ++u)
+#pragma unroll
+      for (int j = 0; j < E / 4; ++j) {
+        sum[4 * j] += x[u][j].x;
+        sum[4 * j + 1] += x[u][j].y;
+        sum[4 * j + 2] += x[u][j].z;
+        sum[4 * j + 3] += x[u][j].w;
+      }
+  }
+}
+
+// The long runs that start among a CTA's kJoinWarps * 32 items, on one slab. A
+// run of up to kAlone parts is one warp's, the warps take turns; more parts
+// are shared by all warps.
+constexpr int kJoinWarps = 8, kJoinItems = kJoinWarps * 32, kAlone = 16;
+template <typename TI, typename TO, bool kVec>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(GradArgs a) {
+  constexpr int E = kLane<TI>;
+  __shared__ float s_part[kJoinWarps][E][32];
+  __shared__ int4 s_run[kJoinItems / kShort + 1];     // token, first window, parts
+  __shared__ int s_runs;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int block = blockIdx.x / a.slabs, slab = blockIdx.x - block * a.slabs, col = slab * kSlab<TI>;
+  const int pos = block * kJoinItems + tid;
+  if (tid == 0) s_runs = 0;
   __syncthreads();
-  if (w != 0) return;
-  // the warps' parts in order: equal tokens are one run
-  const int piece_end = min(N, p0 + kPiece);
-  int token = -1, begin = 0, end = 0;
-#pragma unroll
-  for (int q = 0; q < kQuads; ++q) sum[q] = make_float4(0, 0, 0, 0);
-  const long long row = static_cast<long long>(a.slabs) * kQuads * kSlab / 4;
-  auto flush = [&]() {
-    if (token < 0) return;
-    if (begin < p0 || end > piece_end) {
-      float4* parts = reinterpret_cast<float4*>(a.parts + col0) + lane;
-#pragma unroll
-      for (int q = 0; q < kQuads; ++q)
-        __stcg(parts + (2ll * piece + (begin < p0 ? 0 : 1)) * row + q * kSlab / 4, sum[q]);
-      const int first = begin / kPiece, last = (end - 1) / kPiece;
-      __threadfence();
-      __syncwarp();
-      unsigned before = 0;
-      if (lane == 0) before = atom_add_acq_rel_gpu(a.arrived + static_cast<long long>(first) * a.slabs + slab, 1u);
-      before = __shfl_sync(0xffffffffu, before, 0);
-      if (before != static_cast<unsigned>(last - first)) return;
-      __threadfence();
-#pragma unroll
-      for (int q = 0; q < kQuads; ++q) {
-        const float4* from = parts + q * kSlab / 4;
-        sum[q] = __ldcg(from + (2ll * first + 1) * row);
-        int g = first + 1;
-        for (; g + 8 <= last + 1; g += 8) {
-          float4 x[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) x[u] = __ldcg(from + 2ll * (g + u) * row);
-#pragma unroll
-          for (int u = 0; u < 8; ++u) sum[q] = plus(sum[q], x[u]);
-        }
-        for (; g <= last; ++g) sum[q] = plus(sum[q], __ldcg(from + 2ll * g * row));
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < kQuads; ++q) finish<TO, kVec>(a, token, col0 + q * kSlab, lane, sum[q]);
-  };
-  for (int j = 0; j < kSumWarps * 2; ++j) {
-    const int4 run = s_run[j >> 1][j & 1];
-    if (run.x < 0) continue;
-    if (run.x != token) {
-      flush();
-      token = run.x;
-      begin = run.y;
-      end = run.z;
-#pragma unroll
-      for (int q = 0; q < kQuads; ++q) sum[q] = make_float4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int q = 0; q < kQuads; ++q) sum[q] = plus(sum[q], s_part[j >> 1][j & 1][q][lane]);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int4 it = make_int4(0, 0, 0, 0);
+  if (pos < a.n) it = __ldcg(a.sorted + pos);
+  const bool start = pos < __ldcg(a.n_sorted) && pos == it.z && it.w - it.z > kShort;
+  if (start)      // at most one in every kShort + 1 items; the order does not matter
+    s_run[atomicAdd(&s_runs, 1)] = make_int4(it.y, pos / kWindow, (it.w - 1) / kWindow - pos / kWindow + 1, 0);
+  __syncthreads();
+  const int runs = s_runs;
+  float sum[E];
+  for (int j = w; j < runs; j += kJoinWarps) {
+    const int4 run = s_run[j];
+    if (run.z > kAlone) continue;
+    clear(sum);
+    add_parts<E>(a, run.y, 0, run.z, slab, lane, sum);
+    finish<TO, kVec>(a, run.x, col, lane, sum);
   }
-  flush();
+  for (int j = 0; j < runs; ++j) {
+    const int4 run = s_run[j];
+    if (run.z <= kAlone) continue;
+    const int per = ceil_div(run.z, kJoinWarps), p0 = min(run.z, w * per), p1 = min(run.z, p0 + per);
+    clear(sum);
+    add_parts<E>(a, run.y, p0, p1, slab, lane, sum);
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_part[w][e][lane] = sum[e];
+    __syncthreads();
+    if (w == 0) {
+      for (int g = 1; g < kJoinWarps; ++g)
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[e] += s_part[g][e][lane];
+      finish<TO, kVec>(a, run.x, col, lane, sum);
+    }
+    __syncthreads();
+  }
 }
 
 // One CTA an item and up to kDirectWarps slabs; the CTA of a token's first
 // item sums all of that token's items. Its warps share the slabs and, where
 // there are fewer slabs than warps, the items in equal parts.
+constexpr int kZeroThreads = 512;
+__global__ void __launch_bounds__(kZeroThreads) zero_kernel(uint4* d, long long vecs, uint16_t* rest, int halves) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const long long step = static_cast<long long>(gridDim.x) * kZeroThreads;
+  for (long long i = static_cast<long long>(blockIdx.x) * kZeroThreads + threadIdx.x; i < vecs; i += step)
+    d[i] = make_uint4(0, 0, 0, 0);
+  if (blockIdx.x == 0 && threadIdx.x < halves) rest[threadIdx.x] = 0;
+}
+
 template <typename TI, typename TO, bool kVec>
 __global__ void __launch_bounds__(kDirectThreads) direct_kernel(GradArgs a) {
-  constexpr int kLoads = kDirectItems / kDirectThreads;
+  constexpr int kLoads = kDirectItems / kDirectThreads, E = kLane<TI>;
   __shared__ unsigned s_hits[kDirectItems / 32];
   __shared__ short s_items[kDirectItems];
-  __shared__ float4 s_sum[kDirectWarps][32];
+  __shared__ float s_sum[kDirectWarps][E][32];
   const int i = blockIdx.x, tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  // zero_kernel is done; every CTA waits, so that the grid ends after it
+  auto zeroed = [&]() {
+    if (!a.accumulate) asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
   int mine[kLoads];
 #pragma unroll
   for (int u = 0; u < kLoads; ++u) {
@@ -532,6 +688,7 @@ __global__ void __launch_bounds__(kDirectThreads) direct_kernel(GradArgs a) {
   const int t = __ldg(a.tokens + i);
   if (t < 0 || t >= a.V) {
     if (t != -1 && tid == 0 && blockIdx.y == 0) record_bad_token(a.err, i);
+    zeroed();
     return;
   }
   bool before = false;
@@ -541,7 +698,10 @@ __global__ void __launch_bounds__(kDirectThreads) direct_kernel(GradArgs a) {
     const unsigned mask = __ballot_sync(0xffffffffu, mine[u] == t);
     if (lane == 0) s_hits[u * kDirectWarps + w] = mask;
   }
-  if (__syncthreads_or(before)) return;
+  if (__syncthreads_or(before)) {
+    zeroed();
+    return;
+  }
   // the token's items in order
   const unsigned word = s_hits[lane];
   int at = __popc(word);
@@ -557,50 +717,53 @@ __global__ void __launch_bounds__(kDirectThreads) direct_kernel(GradArgs a) {
   __syncthreads();
   const int here = min(kDirectWarps, a.slabs - static_cast<int>(blockIdx.y) * kDirectWarps);   // slabs of this CTA
   const int groups = kDirectWarps / here;
-  const int group = w / here, col = (static_cast<int>(blockIdx.y) * kDirectWarps + w % here) * kSlab;
+  const int group = w / here, col = (static_cast<int>(blockIdx.y) * kDirectWarps + w % here) * kSlab<TI>;
+  float sum[E];
+  clear(sum);
   if (group < groups) {
     const int per = ceil_div(total, groups), lo = min(total, group * per), hi = min(total, lo + per);
     const TI* dout = static_cast<const TI*>(a.dout) + col;
-    float4 sum = make_float4(0, 0, 0, 0);
-    constexpr int kRowsAhead = 8;
-    for (int j = lo; j < hi; j += kRowsAhead) {
-      float4 x[kRowsAhead];
+    for (int j = lo; j < hi; j += kAhead) {
+      uint4 x[kAhead];
 #pragma unroll
-      for (int u = 0; u < kRowsAhead; ++u)
-        x[u] = j + u < hi ? load_quad<TI, kVec>(dout + static_cast<long long>(s_items[j + u]) * a.r, lane, a.r - col)
-                          : make_float4(0, 0, 0, 0);
+      for (int u = 0; u < kAhead; ++u)
+        x[u] = j + u < hi ? load_lane<TI, kVec>(dout + static_cast<long long>(s_items[j + u]) * a.r, lane, a.r - col)
+                          : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int u = 0; u < kRowsAhead; ++u) sum = plus(sum, x[u]);
+      for (int u = 0; u < kAhead; ++u) add_lane(sum, x[u]);
     }
-    s_sum[w][lane] = sum;
+    if (group > 0)
+#pragma unroll
+      for (int j = 0; j < E; ++j) s_sum[w][j][lane] = sum[j];
   }
   __syncthreads();
+  zeroed();
   if (w >= here) return;
-  float4 sum = s_sum[w][lane];
-  for (int g = 1; g < groups; ++g) sum = plus(sum, s_sum[g * here + w][lane]);
+  for (int g = 1; g < groups; ++g)
+#pragma unroll
+    for (int j = 0; j < E; ++j) sum[j] += s_sum[g * here + w][j][lane];
   finish<TO, kVec>(a, t, col, lane, sum);
 }
 
-// Sizes of the two-kernel path for (n, V, r) with slabs of `quads` quads, and
-// its scratch.
+// Sizes of the sorted path for (n, V, r) and rows of dout of `lane_cols`
+// columns a lane, and its scratch.
 struct GradPlan {
-  int R, owners, slabs, P, pieces;
-  size_t smem, off_n, off_arrived, off_sorted, off_parts, bytes;
+  int R, owners, keep, slabs, pieces;
+  size_t smem, off_n, off_sorted, off_parts, bytes;
 };
-GradPlan grad_plan(int n, int V, int r, int quads) {
+GradPlan grad_plan(int n, int V, int r, int lane_cols) {
+  constexpr int kSmemWords = (224 << 10) / 4;
   GradPlan p{};
   p.R = std::min(kMaxR, ceil_div(V, kMaxSms));
   p.owners = ceil_div(V, p.R);
-  p.slabs = ceil_div(r, quads * kSlab);
-  // 32 items a warp where that still makes four CTAs an SM, else 8
-  p.P = static_cast<long long>(n) * p.slabs >= 4ll * kMaxSms * kSumWarps * 32 ? 32 : 8;
-  p.pieces = std::max(1, ceil_div(n, kSumWarps * p.P));
-  p.smem = static_cast<size_t>(kSortWarps * p.R + p.R + kSortWarps * kKeep) * sizeof(unsigned);
+  p.keep = std::min((kSmemWords - 256 - (kSortWarps + 2) * p.R) / kSortWarps, std::max(32, ceil_div(n, kSortWarps)));
+  p.slabs = ceil_div(r, 32 * lane_cols);
+  p.pieces = std::max(1, ceil_div(n, kPiece));
+  p.smem = (static_cast<size_t>(kSortWarps + 2) * p.R + static_cast<size_t>(kSortWarps) * p.keep) * sizeof(unsigned);
   p.off_n = kScratchOffset;
-  p.off_arrived = p.off_n + 256;
-  p.off_sorted = align_up(p.off_arrived + static_cast<size_t>(p.pieces) * p.slabs * sizeof(unsigned), 256);
+  p.off_sorted = p.off_n + 256;
   p.off_parts = align_up(p.off_sorted + static_cast<size_t>(n) * sizeof(int4), 256);
-  p.bytes = align_up(p.off_parts + static_cast<size_t>(p.pieces) * 2 * p.slabs * quads * kSlab * sizeof(float), 256);
+  p.bytes = align_up(p.off_parts + static_cast<size_t>(p.pieces) * kSumWarps * 2 * p.slabs * 32 * lane_cols * sizeof(float), 256);
   return p;
 }
 
@@ -611,52 +774,64 @@ bool embed_sizes_ok(int n, int V, int r) {
   return n >= 0 && n <= kMaxItems && V >= 1 && V <= kMaxV && r >= 1 && r <= DSPARK_MAX_EMBED_R;
 }
 
-template <typename TI, typename TO, bool kVec, int kQuads>
-cudaError_t launch_sorted(GradArgs a, char* ws, cudaStream_t s) {
-  const GradPlan p = grad_plan(a.n, a.V, a.r, kQuads);
-  a.R = p.R;
+template <typename TI, typename TO, bool kVec>
+cudaError_t launch_grad(GradArgs a, char* ws, cudaStream_t s) {
+  const GradPlan p = grad_plan(a.n, a.V, a.r, kLane<TI>);
   a.slabs = p.slabs;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.accumulate ? 0 : 1;
+  if (a.n <= kDirectItems) {
+    if (!a.accumulate) {
+      const long long bytes = static_cast<long long>(a.V) * a.r * static_cast<long long>(sizeof(TO));
+      char* d = static_cast<char*>(a.dtable);
+      const long long vecs = bytes / 16;
+      const int grid = static_cast<int>(std::max(1ll, std::min<long long>(2 * kMaxSms, (vecs + kZeroThreads - 1) / kZeroThreads)));
+      zero_kernel<<<grid, kZeroThreads, 0, s>>>(reinterpret_cast<uint4*>(d), vecs,
+                                                reinterpret_cast<uint16_t*>(d + vecs * 16),
+                                                static_cast<int>(bytes - vecs * 16) / 2);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
+    if (a.n == 0) return cudaSuccess;
+    cfg.gridDim = dim3(a.n, ceil_div(a.slabs, kDirectWarps));
+    cfg.blockDim = dim3(kDirectThreads);
+    return cudaLaunchKernelEx(&cfg, direct_kernel<TI, TO, kVec>, a);
+  }
+  a.R = p.R;
+  a.keep = p.keep;
   a.pieces = p.pieces;
   a.n_sorted = reinterpret_cast<int*>(ws + p.off_n);
-  a.arrived = reinterpret_cast<unsigned*>(ws + p.off_arrived);
   a.sorted = reinterpret_cast<int4*>(ws + p.off_sorted);
   a.parts = reinterpret_cast<float*>(ws + p.off_parts);
   cudaError_t e = cudaFuncSetAttribute(sort_kernel<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(p.smem));
   if (e != cudaSuccess) return e;
-  sort_kernel<TO><<<p.owners, kSortThreads, p.smem, s>>>(a);
+  sort_kernel<TO><<<p.owners, (a.accumulate ? 1 : 2) * kSortThreads, p.smem, s>>>(a);
   e = cudaGetLastError();
-  if (e != cudaSuccess || a.n == 0) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
+  if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(p.pieces * p.slabs);
   cfg.blockDim = dim3(kSumThreads);
-  cfg.stream = s;
-  cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(
-      &cfg, p.P == 32 ? sum_kernel<TI, TO, kVec, kQuads, 32> : sum_kernel<TI, TO, kVec, kQuads, 8>, a);
-}
-
-template <typename TI, typename TO, bool kVec>
-cudaError_t launch_grad(GradArgs a, char* ws, cudaStream_t s) {
-  if (a.accumulate && a.n <= kDirectItems) {
-    if (a.n == 0) return cudaSuccess;
-    a.slabs = ceil_div(a.r, kSlab);
-    direct_kernel<TI, TO, kVec><<<dim3(a.n, ceil_div(a.slabs, kDirectWarps)), kDirectThreads, 0, s>>>(a);
-    return cudaGetLastError();
-  }
-  // two quads a lane keep as many bytes in flight for bf16 as one for fp32
-  if constexpr (sizeof(TI) == 2)
-    if (a.r > kSlab) return launch_sorted<TI, TO, kVec, 2>(a, ws, s);
-  return launch_sorted<TI, TO, kVec, 1>(a, ws, s);
+  auto sum = a.accumulate ? sum_kernel<TI, TO, kVec, true> : sum_kernel<TI, TO, kVec, false>;
+  cfg.dynamicSmemBytes = a.accumulate ? sizeof(SumShared<TI, TO, true>) : sizeof(SumShared<TI, TO, false>);
+  e = cudaFuncSetAttribute(sum, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(cfg.dynamicSmemBytes));
+  if (e != cudaSuccess) return e;
+  e = cudaLaunchKernelEx(&cfg, sum, a);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(ceil_div(a.n, kJoinItems) * p.slabs);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, join_kernel<TI, TO, kVec>, a);
 }
 
 template <typename TI, typename TO>
 cudaError_t launch_grad(const GradArgs& a, char* ws, cudaStream_t s) {
-  return a.r % 4 == 0 ? launch_grad<TI, TO, true>(a, ws, s) : launch_grad<TI, TO, false>(a, ws, s);
+  return a.r % kLane<TI> == 0 ? launch_grad<TI, TO, true>(a, ws, s) : launch_grad<TI, TO, false>(a, ws, s);
 }
 
 }  // namespace
@@ -684,7 +859,7 @@ dspark_status dspark_embed(const void* table, dspark_dtype table_dtype, const in
 }
 
 size_t dspark_embed_grad_workspace_bytes(int n, int V, int r) {
-  return embed_sizes_ok(n, V, r) ? std::max(grad_plan(n, V, r, 1).bytes, grad_plan(n, V, r, 2).bytes) : 0;
+  return embed_sizes_ok(n, V, r) ? std::max(grad_plan(n, V, r, 4).bytes, grad_plan(n, V, r, 8).bytes) : 0;
 }
 
 dspark_status dspark_embed_grad(const void* dout, dspark_dtype dout_dtype, const int32_t* tokens, int n, int V, int r,
