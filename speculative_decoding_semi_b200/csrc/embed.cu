@@ -166,8 +166,9 @@ cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t s) {
 // sum_kernel: the sorted items in windows of equal length, one a warp. A short
 //   run of equal tokens is summed by the warp in whose window it starts. A
 //   longer one is summed by all whose windows it touches, so that a frequent
-//   token does not hold up one CTA; their parts go to scratch.
-// join_kernel: adds the parts of each long run in order.
+//   token does not hold up one warp or CTA: a CTA joins its warps' parts in
+//   shared memory, and those of a run that goes on go to scratch.
+// join_kernel: adds the CTAs' parts of each such run in order.
 //
 // Few items: direct_kernel, one CTA an item, no sorting; without accumulate it
 // runs beside zero_kernel and waits for it before it writes.
@@ -184,14 +185,14 @@ struct GradArgs {
   int keep;               // matches that a warp of the sort keeps in shared memory; more are found again
   int* n_sorted;          // items with a token
   int4* sorted;           // [n] item, token, and the run [begin, end) it is in
-  float* parts;           // [windows][2][slabs][32 lanes]: of the long run that comes in, of the one that starts
+  float* parts;           // [pieces][2][slabs][32 lanes]: of the long run that comes in, of the one that leaves
 };
 
 constexpr int kSortWarps = 16, kSortThreads = kSortWarps * 32;
 constexpr int kMaxR = 2048;     // rows of an owner (11 bits beside 20 of an item's place in a warp's piece)
 constexpr int kWindow = 16;     // sorted items of a warp
 constexpr int kShort = 16;      // a run up to this length belongs to one warp (kWindow + kShort <= 32)
-constexpr int kAhead = 8;       // rows of a warp in flight
+constexpr int kAhead = 6;       // rows of a warp in flight
 constexpr int kSumWarps = 8, kSumThreads = kSumWarps * 32, kPiece = kSumWarps * kWindow;
 constexpr int kDirectItems = 1024;
 constexpr int kDirectWarps = 8, kDirectThreads = kDirectWarps * 32;
@@ -275,15 +276,14 @@ __global__ void __launch_bounds__(2 * kSortThreads, 1) sort_kernel(GradArgs a) {
       const int i = i0 + u * 128 + lane * 4;
       const int t[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
       bool hit[4];
-      bool any = false, bad = false;
+      bool any = false;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        bad |= t[c] < -1 || t[c] >= a.V;
-        below += t[c] >= 0 && t[c] < v0;
-        hit[c] = t[c] >= v0 && t[c] < v0 + rows;
+      for (int c = 0; c < 4; ++c) {           // -1 and bad ids are in no range
+        below += static_cast<unsigned>(t[c]) < static_cast<unsigned>(v0);
+        hit[c] = static_cast<unsigned>(t[c] - v0) < static_cast<unsigned>(rows);
         any |= hit[c];
       }
-      if (bad && blockIdx.x == 0)
+      if (blockIdx.x == 0)
         for (int c = 0; c < 4; ++c)
           if (t[c] < -1 || t[c] >= a.V) record_bad_token(a.err, i + c);
       if (__ballot_sync(0xffffffffu, any) == 0u) continue;
@@ -472,120 +472,188 @@ __device__ __forceinline__ void finish(const GradArgs& a, int token, int col, in
   save_lane<TO, kVec, E>(d, lane, cols, v);
 }
 
-// A lane's columns (16 bytes of TI) of a row to its place in shared memory,
-// without waiting; where the rows are not aligned, by way of registers.
+// A warp's columns of a row to shared memory, without waiting: where the rows
+// are aligned each lane copies its own columns and later reads those; else the
+// row's 16-byte blocks are copied, from the one that holds the first column
+// on, and a lane reads columns 32 apart, the first `skew` bytes into the place.
 template <typename T, bool kVec, int E>
-__device__ __forceinline__ void fetch_lane(T* to, const T* p, int lane, int cols) {
-  constexpr int kBytes = E * static_cast<int>(sizeof(T)), kStep = kBytes < 16 ? kBytes : 16;
-  if constexpr (kVec) {
-    if (lane * E < cols) {
-      const unsigned at = static_cast<unsigned>(__cvta_generic_to_shared(to));
+struct Place {
+  static constexpr int kBytes = 32 * E * static_cast<int>(sizeof(T));
+  static constexpr int kSize = kVec ? kBytes : kBytes + 16;
+  __device__ __forceinline__ static void fetch(char* to, const T* p, int lane, int cols) {
+    unsigned at = static_cast<unsigned>(__cvta_generic_to_shared(to));
+    if constexpr (kVec) {
+      constexpr int kMine = E * static_cast<int>(sizeof(T)), kStep = kMine < 16 ? kMine : 16;
+      if (lane * E < cols) {
 #pragma unroll
-      for (int j = 0; j < kBytes; j += kStep)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at + j),
-                     "l"(reinterpret_cast<const char*>(p + lane * E) + j), "n"(kStep)
+        for (int j = 0; j < kMine; j += kStep)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at + lane * kMine + j),
+                       "l"(reinterpret_cast<const char*>(p) + lane * kMine + j), "n"(kStep)
+                       : "memory");
+      }
+    } else {
+      const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
+      const int bytes = skew + min(cols, 32 * E) * static_cast<int>(sizeof(T));
+      const char* from = reinterpret_cast<const char*>(p) - skew;
+      for (int j = lane * 16; j < bytes; j += 512)      // the last block up to the row's end only
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(at + j), "l"(from + j), "r"(min(16, bytes - j))
                      : "memory");
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < E; ++j)
-      if (lane + 32 * j < cols) to[j] = p[lane + 32 * j];
   }
-}
-
-template <typename TI, typename TO, bool kAdd>
-struct SumShared {
-  static constexpr int E = kLane<TI>;
-  struct __align__(16) In {
-    TI v[E];
-  };
-  struct __align__(16) Old {
-    TO v[E];
-  };
-  In rows[kSumWarps][kAhead][32];
-  Old old[kAdd ? kSumWarps : 1][kAdd ? kAhead : 1][32];
+  // Adds the lane's columns, once its copies (kVec) or the warp's are there.
+  __device__ __forceinline__ static void add(float (&s)[E], const char* place, const T* p, int lane) {
+    if constexpr (kVec) {
+      const T* v = reinterpret_cast<const T*>(place) + lane * E;
+      if constexpr (sizeof(T) * E == 16) {
+        add_lane(s, *reinterpret_cast<const uint4*>(v));
+      } else if constexpr (sizeof(T) == 2) {
+        const uint2 x = *reinterpret_cast<const uint2*>(v);
+        s[0] += __uint_as_float(x.x << 16), s[1] += __uint_as_float(x.x & 0xffff0000u);
+        s[2] += __uint_as_float(x.y << 16), s[3] += __uint_as_float(x.y & 0xffff0000u);
+      } else {
+#pragma unroll
+        for (int j = 0; j < E; j += 4) {
+          const float4 x = reinterpret_cast<const float4*>(v)[j / 4];
+          s[j] += x.x, s[j + 1] += x.y, s[j + 2] += x.z, s[j + 3] += x.w;
+        }
+      }
+    } else {
+      const T* v = reinterpret_cast<const T*>(place + (reinterpret_cast<uintptr_t>(p) & 15u)) + lane;
+#pragma unroll
+      for (int j = 0; j < E; ++j) s[j] += to_float(v[32 * j]);     // columns behind the row: not saved
+    }
+  }
 };
 
-// A lane's place in the scratch for window g's part of a long run: the run
-// that comes in (k = 0), or starts there (1).
+template <typename TI, typename TO, bool kVec, bool kAdd>
+struct SumShared {
+  static constexpr int E = kLane<TI>;
+  alignas(16) char rows[kSumWarps][kAhead][Place<TI, kVec, E>::kSize];
+  alignas(16) char old[kAdd ? kSumWarps : 1][kAdd ? kAhead : 1][Place<TO, kVec, E>::kSize];
+  float part[kSumWarps][2][E][32];
+  int4 run[kSumWarps][2];   // token, begin, end of each long run's part; token -1: none
+  int4 list[kSumWarps][32];
+};
+
+// A lane's place in the scratch for piece g's part of a long run: the run that
+// comes in (k = 0), or starts there and leaves (1).
 template <int E>
 __device__ __forceinline__ float4* part_of(const GradArgs& a, int g, int k, int slab, int lane) {
   return reinterpret_cast<float4*>(a.parts) + (((2ll * g + k) * a.slabs + slab) * 32 + lane) * (E / 4);
 }
 
-// A warp is on its own: one window, one slab.
+// A window a warp, on one slab; the long runs' parts are joined in the CTA.
 template <typename TI, typename TO, bool kVec, bool kAdd>
-__global__ void __launch_bounds__(kSumThreads, kAdd ? 2 : 4) sum_kernel(GradArgs a) {
+__global__ void __launch_bounds__(kSumThreads, kAdd ? 2 : 5) sum_kernel(GradArgs a) {
   constexpr int E = kLane<TI>;
   extern __shared__ __align__(16) unsigned char sum_smem[];
-  SumShared<TI, TO, kAdd>& sh = *reinterpret_cast<SumShared<TI, TO, kAdd>*>(sum_smem);
+  SumShared<TI, TO, kVec, kAdd>& sh = *reinterpret_cast<SumShared<TI, TO, kVec, kAdd>*>(sum_smem);
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int piece = blockIdx.x / a.slabs, slab = blockIdx.x - piece * a.slabs;
-  const int window = piece * kSumWarps + w, lo = window * kWindow, pos = lo + lane;
+  const int p0 = piece * kPiece, lo = p0 + w * kWindow, pos = lo + lane;
   const int col = slab * kSlab<TI>, cols = a.r - col;
+  if (lane < 2) sh.run[w][lane].x = -1;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // what lies behind the last sorted item is read but not used
   int4 it = make_int4(0, 0, 0, 0);
   if (pos < a.n) it = __ldcg(a.sorted + pos);
   const int N = __ldcg(a.n_sorted), hi = min(N, lo + kWindow);
-  if (lo >= N) return;
-  const bool is_short = it.w - it.z <= kShort;
-  const bool mine = pos < N && (is_short ? it.z >= lo && it.z < hi : pos < hi);
-  unsigned left = __ballot_sync(0xffffffffu, mine);
-  const unsigned ends = __ballot_sync(0xffffffffu, mine && (pos == it.w - 1 || (!is_short && pos == hi - 1)));
-  const unsigned shorts = __ballot_sync(0xffffffffu, is_short);
+  if (p0 >= N) return;
+  // the warp's items, moved together: lane j then holds the j-th
+  unsigned ends, shorts;
+  int items;
+  {
+    const bool is_short = it.w - it.z <= kShort;
+    const bool mine = pos < N && (is_short ? it.z >= lo && it.z < hi : pos < hi);
+    const bool is_end = pos == it.w - 1 || (!is_short && pos == hi - 1);
+    const unsigned mask = __ballot_sync(0xffffffffu, mine);
+    items = __popc(mask);
+    if (mine)
+      sh.list[w][__popc(mask & ((1u << lane) - 1u))] =
+          make_int4(it.x | (is_end ? 1 << 30 : 0) | (is_short ? 1 << 29 : 0), it.y, it.z, it.w);
+    __syncwarp();
+    it = sh.list[w][lane];      // behind the last item: not used
+    ends = __ballot_sync(0xffffffffu, lane < items && (it.x >> 30 & 1) != 0);
+    shorts = __ballot_sync(0xffffffffu, (it.x >> 29 & 1) != 0);
+    it.x &= (1 << 29) - 1;
+  }
   const TI* dout = static_cast<const TI*>(a.dout) + col;
   TO* dtable = static_cast<TO*>(a.dtable) + col;
   float sum[E];
   clear(sum);
-  while (left != 0u) {
-    unsigned todo = left;
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int at = __ffs(todo) - 1;
-      const int item = __shfl_sync(0xffffffffu, it.x, at & 31), token = __shfl_sync(0xffffffffu, it.y, at & 31);
-      if (todo != 0u) {
-        fetch_lane<TI, kVec, E>(sh.rows[w][u][lane].v, dout + static_cast<long long>(item) * a.r, lane, cols);
-        if (kAdd && ((ends & shorts) >> at & 1u) != 0u)      // what the run's sum is added to
-          fetch_lane<TO, kVec, E>(sh.old[kAdd ? w : 0][kAdd ? u : 0][lane].v,
-                                  dtable + static_cast<long long>(token) * a.r, lane, cols);
+  // rows go through a ring of kAhead places; each lane reads what it copied
+  auto fetch = [&](int j, int u) {
+    if (j < items) {
+      const int item = __shfl_sync(0xffffffffu, it.x, j);
+      Place<TI, kVec, E>::fetch(sh.rows[w][u], dout + static_cast<long long>(item) * a.r, lane, cols);
+      if (kAdd && ((ends & shorts) >> j & 1u) != 0u) {     // what the run's sum is added to
+        const int token = __shfl_sync(0xffffffffu, it.y, j);
+        Place<TO, kVec, E>::fetch(sh.old[kAdd ? w : 0][kAdd ? u : 0], dtable + static_cast<long long>(token) * a.r, lane,
+                                  cols);
       }
-      todo &= todo - 1;
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) fetch(u, u);
+  int u = 0;
 #pragma unroll 1
-    for (int u = 0; u < kAhead && left != 0u; ++u) {
-      const int at = __ffs(left) - 1;
-      left &= left - 1;
+  for (int j = 0; j < items; ++j) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    if (!kVec) __syncwarp();      // the other lanes' copies
+    Place<TI, kVec, E>::add(sum, sh.rows[w][u],
+                            kVec ? dout : dout + static_cast<long long>(__shfl_sync(0xffffffffu, it.x, j)) * a.r, lane);
+    if ((ends >> j & 1u) != 0u) {
+      const int token = __shfl_sync(0xffffffffu, it.y, j);
+      if ((shorts >> j & 1u) != 0u) {
 #pragma unroll
-      for (int j = 0; j < E; ++j) sum[j] += to_float(sh.rows[w][u][lane].v[j]);
-      if ((ends >> at & 1u) == 0u) continue;
-      if ((shorts >> at & 1u) != 0u) {
-        const int token = __shfl_sync(0xffffffffu, it.y, at);
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          sum[j] *= a.scale;
-          if (kAdd) sum[j] += to_float(sh.old[kAdd ? w : 0][kAdd ? u : 0][lane].v[j]);
-        }
-        save_lane<TO, kVec, E>(dtable + static_cast<long long>(token) * a.r, lane, cols, sum);
+        for (int e = 0; e < E; ++e) sum[e] *= a.scale;
+        TO* d = dtable + static_cast<long long>(token) * a.r;
+        if constexpr (kAdd) Place<TO, kVec, E>::add(sum, sh.old[w][u], d, lane);
+        save_lane<TO, kVec, E>(d, lane, cols, sum);
       } else {
         // a long run's part: it came in, or starts here (and leaves: it is longer than a window)
-        float4* part = part_of<E>(a, window, __shfl_sync(0xffffffffu, it.z, at) < lo ? 0 : 1, slab, lane);
+        const int begin = __shfl_sync(0xffffffffu, it.z, j), end = __shfl_sync(0xffffffffu, it.w, j);
+        const int k = begin < lo ? 0 : 1;
+        if (lane == 0) sh.run[w][k] = make_int4(token, begin, end, 0);
 #pragma unroll
-        for (int j = 0; j < E / 4; ++j)
-          part[j] = make_float4(sum[4 * j], sum[4 * j + 1], sum[4 * j + 2], sum[4 * j + 3]);
+        for (int e = 0; e < E; ++e) sh.part[w][k][e][lane] = sum[e];
       }
       clear(sum);
+    }
+    if (!kVec) __syncwarp();      // the place is read
+    fetch(j + kAhead, u);
+    u = u == kAhead - 1 ? 0 : u + 1;
+  }
+  if (!__syncthreads_or((ends & ~shorts) != 0u)) return;
+  // The first part of a run here is one that starts in a window, or comes into
+  // the piece: the warp of that window adds the parts behind it.
+  for (int k = w == 0 ? 0 : 1; k < 2; ++k) {
+    const int4 run = sh.run[w][k];
+    if (run.x < 0) continue;
+    const int stop = min((run.z - 1 - p0) / kWindow, kSumWarps - 1);   // the last window it touches
+    clear(sum);
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[e] = sh.part[w][k][e][lane];
+    for (int i = w + 1; i <= stop; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum[e] += sh.part[i][0][e][lane];
+    if (run.y >= p0 && run.z <= p0 + kPiece) {
+      finish<TO, kVec>(a, run.x, col, lane, sum);
+    } else {
+      float4* part = part_of<E>(a, piece, run.y < p0 ? 0 : 1, slab, lane);
+#pragma unroll
+      for (int e = 0; e < E / 4; ++e) part[e] = make_float4(sum[4 * e], sum[4 * e + 1], sum[4 * e + 2], sum[4 * e + 3]);
     }
   }
 }
 
-// Adds parts [lo, hi) of the long run whose parts start at window `first`.
+// Adds parts [lo, hi) of the run whose parts start at piece `first`.
 template <int E>
 __device__ __forceinline__ void add_parts(const GradArgs& a, int first, int lo, int hi, int slab, int lane,
                                           float (&sum)[E]) {
-  constexpr int kParts = 32 / E;
+  constexpr int kParts = 64 / E;
   for (int g = lo; g < hi; g += kParts) {
     float4 x[kParts][E / 4];
 #pragma unroll
@@ -606,43 +674,38 @@ __device__ __forceinline__ void add_parts(const GradArgs& a, int first, int lo, 
   }
 }
 
-// The long runs that start among a CTA's kJoinWarps * 32 items, on one slab. A
-// run of up to kAlone parts is one warp's, the warps take turns; more parts
-// are shared by all warps.
-constexpr int kJoinWarps = 8, kJoinItems = kJoinWarps * 32, kAlone = 16;
+// The runs that leave a piece, a warp a piece and slab: the run that holds the
+// piece's last item, if it starts in the piece and goes on. One of up to
+// kAlone parts is the warp's, more are shared by all warps of the CTA.
+constexpr int kJoinWarps = 8;
 template <typename TI, typename TO, bool kVec>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(GradArgs a) {
-  constexpr int E = kLane<TI>;
+  constexpr int E = kLane<TI>, kAlone = 64 / E;
   __shared__ float s_part[kJoinWarps][E][32];
-  __shared__ int4 s_run[kJoinItems / kShort + 1];     // token, first window, parts
-  __shared__ int s_runs;
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  __shared__ int2 s_run[kJoinWarps];     // token, parts (more than kAlone, or 0)
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int block = blockIdx.x / a.slabs, slab = blockIdx.x - block * a.slabs, col = slab * kSlab<TI>;
-  const int pos = block * kJoinItems + tid;
-  if (tid == 0) s_runs = 0;
-  __syncthreads();
+  const int piece = block * kJoinWarps + w, last = (piece + 1) * kPiece - 1;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   int4 it = make_int4(0, 0, 0, 0);
-  if (pos < a.n) it = __ldcg(a.sorted + pos);
-  const bool start = pos < __ldcg(a.n_sorted) && pos == it.z && it.w - it.z > kShort;
-  if (start)      // at most one in every kShort + 1 items; the order does not matter
-    s_run[atomicAdd(&s_runs, 1)] = make_int4(it.y, pos / kWindow, (it.w - 1) / kWindow - pos / kWindow + 1, 0);
-  __syncthreads();
-  const int runs = s_runs;
+  if (last < a.n) it = __ldcg(a.sorted + last);
+  const int N = __ldcg(a.n_sorted);
+  const bool leaves = last < N && it.w - it.z > kShort && it.z >= piece * kPiece && it.w > last + 1;
+  const int parts = leaves ? (it.w - 1) / kPiece - piece + 1 : 0;
   float sum[E];
-  for (int j = w; j < runs; j += kJoinWarps) {
-    const int4 run = s_run[j];
-    if (run.z > kAlone) continue;
+  if (parts > 0 && parts <= kAlone) {
     clear(sum);
-    add_parts<E>(a, run.y, 0, run.z, slab, lane, sum);
-    finish<TO, kVec>(a, run.x, col, lane, sum);
+    add_parts<E>(a, piece, 0, parts, slab, lane, sum);
+    finish<TO, kVec>(a, it.y, col, lane, sum);
   }
-  for (int j = 0; j < runs; ++j) {
-    const int4 run = s_run[j];
-    if (run.z <= kAlone) continue;
-    const int per = ceil_div(run.z, kJoinWarps), p0 = min(run.z, w * per), p1 = min(run.z, p0 + per);
+  if (lane == 0) s_run[w] = make_int2(it.y, parts > kAlone ? parts : 0);
+  if (!__syncthreads_or(parts > kAlone)) return;
+  for (int j = 0; j < kJoinWarps; ++j) {
+    const int2 run = s_run[j];
+    if (run.y == 0) continue;
+    const int per = ceil_div(run.y, kJoinWarps), p0 = min(run.y, w * per), p1 = min(run.y, p0 + per);
     clear(sum);
-    add_parts<E>(a, run.y, p0, p1, slab, lane, sum);
+    add_parts<E>(a, block * kJoinWarps + j, p0, p1, slab, lane, sum);
 #pragma unroll
     for (int e = 0; e < E; ++e) s_part[w][e][lane] = sum[e];
     __syncthreads();
@@ -763,7 +826,7 @@ GradPlan grad_plan(int n, int V, int r, int lane_cols) {
   p.off_n = kScratchOffset;
   p.off_sorted = p.off_n + 256;
   p.off_parts = align_up(p.off_sorted + static_cast<size_t>(n) * sizeof(int4), 256);
-  p.bytes = align_up(p.off_parts + static_cast<size_t>(p.pieces) * kSumWarps * 2 * p.slabs * 32 * lane_cols * sizeof(float), 256);
+  p.bytes = align_up(p.off_parts + static_cast<size_t>(p.pieces) * 2 * p.slabs * 32 * lane_cols * sizeof(float), 256);
   return p;
 }
 
@@ -818,12 +881,13 @@ cudaError_t launch_grad(GradArgs a, char* ws, cudaStream_t s) {
   cfg.blockDim = dim3(kSumThreads);
   cfg.numAttrs = 1;
   auto sum = a.accumulate ? sum_kernel<TI, TO, kVec, true> : sum_kernel<TI, TO, kVec, false>;
-  cfg.dynamicSmemBytes = a.accumulate ? sizeof(SumShared<TI, TO, true>) : sizeof(SumShared<TI, TO, false>);
+  cfg.dynamicSmemBytes = a.accumulate ? sizeof(SumShared<TI, TO, kVec, true>) : sizeof(SumShared<TI, TO, kVec, false>);
   e = cudaFuncSetAttribute(sum, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(cfg.dynamicSmemBytes));
   if (e != cudaSuccess) return e;
   e = cudaLaunchKernelEx(&cfg, sum, a);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(ceil_div(a.n, kJoinItems) * p.slabs);
+  if (a.n <= kPiece) return cudaSuccess;
+  cfg.gridDim = dim3(ceil_div(p.pieces, kJoinWarps) * p.slabs);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, join_kernel<TI, TO, kVec>, a);
