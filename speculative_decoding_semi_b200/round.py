@@ -5,16 +5,18 @@
 synchronisation (the scheduler's verify lengths and row offsets stay on the
 device and feed the verification directly). `run_rounds` chains rounds on the
 device (online temperature calibration and the next anchors included), as a
-plain stream of launches or one captured CUDA graph.
+plain stream of launches or one captured CUDA graph. `TokenScores` holds what a
+reply shows next to the emitted tokens (log probabilities, entropy,
+alternatives under the target); `run_round` fills it when given one.
 """
 from __future__ import annotations
 
 import numpy as np
 import torch
 
-from .binding import (dspark_advance_anchor, dspark_calibrate, dspark_markov_draft, dspark_markov_draft_b,
-                      dspark_rnn_draft, dspark_rnn_draft_b, dspark_schedule, dspark_verify, dspark_verify_b,
-                      dspark_workspace_bytes, dspark_workspace_init)
+from .binding import (dspark_advance_anchor, dspark_calibrate, dspark_logprobs, dspark_markov_draft,
+                      dspark_markov_draft_b, dspark_rnn_draft, dspark_rnn_draft_b, dspark_schedule, dspark_verify,
+                      dspark_verify_b, dspark_workspace_bytes, dspark_workspace_init)
 
 
 def to_device(inputs: dict, device="cuda") -> dict:
@@ -60,6 +62,22 @@ class RoundBuffers:
         dspark_workspace_init(self.workspace)
 
 
+class TokenScores:
+    """Scores of a round's emitted tokens under the target, [B,K+1] as
+    RoundBuffers.out_tokens: log probability, entropy of the distribution the
+    token was drawn from, and the `top_k` most likely tokens with their log
+    probabilities. `stats` is what dspark_logprobs_grad takes."""
+
+    def __init__(self, B: int, K: int, top_k: int = 0, device="cuda"):
+        f32 = torch.float32
+        self.top_k = top_k
+        self.logprob = torch.empty(B, K + 1, dtype=f32, device=device)
+        self.entropy = torch.empty(B, K + 1, dtype=f32, device=device)
+        self.stats = torch.empty(B, K + 1, 2, dtype=f32, device=device)
+        self.top_tokens = torch.empty(B, K + 1, top_k, dtype=torch.int32, device=device) if top_k else None
+        self.top_logprobs = torch.empty(B, K + 1, top_k, dtype=f32, device=device) if top_k else None
+
+
 def draft(d: dict, bufs: RoundBuffers, stream=None, anchor=None):
     """The Markov head, or the RNN head when d holds its recurrent weight "W";
     `anchor` overrides d["anchor"]."""
@@ -98,10 +116,21 @@ def verify(d: dict, bufs: RoundBuffers, target=None, row_start=None, verify_len=
         dspark_verify(target, row_start, bufs.z, *tail)
 
 
-def run_round(d: dict, bufs: RoundBuffers, stream=None):
+def score(d: dict, bufs: RoundBuffers, scores: TokenScores, target=None, row_start=None, stream=None):
+    """Score the emitted tokens (bufs.out_tokens) on the `target` rows that
+    verify drew them from (the same defaults)."""
+    target = d["target"] if target is None else target
+    row_start = d["row_start_dense"] if row_start is None else row_start
+    dspark_logprobs(target, bufs.out_tokens, scores.logprob, scores.entropy, scores.stats, scores.top_tokens,
+                    scores.top_logprobs, bufs.workspace, row_start=row_start, stream=stream)
+
+
+def run_round(d: dict, bufs: RoundBuffers, stream=None, scores: TokenScores | None = None):
     draft(d, bufs, stream)
     schedule(d, bufs, stream)
     verify(d, bufs, stream=stream)
+    if scores is not None:
+        score(d, bufs, scores, stream=stream)
 
 
 class RoundState:
