@@ -440,47 +440,6 @@ __device__ __forceinline__ void add_lane(float (&s)[E], const uint4& v) {
   }
 }
 
-template <int E>
-__device__ __forceinline__ void clear(float (&s)[E]) {
-#pragma unroll
-  for (int j = 0; j < E; ++j) s[j] = 0.f;
-}
-
-template <typename TO, bool kVec, int E>
-__device__ __forceinline__ void save_lane(TO* d, int lane, int cols, const float (&v)[E]) {
-  if constexpr (kVec) {
-    if (lane * E < cols) save_cols<E>(d + lane * E, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < E; ++j)
-      if (lane + 32 * j < cols) store(d + lane + 32 * j, v[j]);
-  }
-}
-
-// dtable[token, a lane's columns from col on] (+)= scale * s
-template <typename TO, bool kVec, int E>
-__device__ __forceinline__ void finish(const GradArgs& a, int token, int col, int lane, const float (&s)[E]) {
-  TO* d = static_cast<TO*>(a.dtable) + static_cast<long long>(token) * a.r + col;
-  const int cols = a.r - col;
-  float v[E];
-#pragma unroll
-  for (int j = 0; j < E; ++j) v[j] = s[j] * a.scale;
-  if (a.accumulate) {
-    float old[E];
-    clear(old);
-    if constexpr (kVec) {
-      if (lane * E < cols) load_cols<E>(d + lane * E, old);
-    } else {
-#pragma unroll
-      for (int j = 0; j < E; ++j)
-        if (lane + 32 * j < cols) old[j] = to_float(d[lane + 32 * j]);
-    }
-#pragma unroll
-    for (int j = 0; j < E; ++j) v[j] += old[j];
-  }
-  save_lane<TO, kVec, E>(d, lane, cols, v);
-}
-
 // A warp's columns of a row to shared memory, without waiting: where the rows
 // are aligned each lane copies its own columns and later reads those; else the
 // row's 16-byte blocks are copied, from the one that holds the first column
@@ -533,6 +492,43 @@ struct Place {
     }
   }
 };
+
+template <int E>
+__device__ __forceinline__ void clear(float (&s)[E]) {
+#pragma unroll
+  for (int j = 0; j < E; ++j) s[j] = 0.f;
+}
+
+template <typename TO, bool kVec, int E>
+__device__ __forceinline__ void save_lane(TO* d, int lane, int cols, const float (&v)[E]) {
+  if constexpr (kVec) {
+    if (lane * E < cols) save_cols<E>(d + lane * E, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (lane + 32 * j < cols) store(d + lane + 32 * j, v[j]);
+  }
+}
+
+// dtable[token, a lane's columns from col on] (+)= scale * s
+template <typename TO, bool kVec, int E>
+__device__ __forceinline__ void finish(const GradArgs& a, int token, int col, int lane, const float (&s)[E]) {
+  TO* d = static_cast<TO*>(a.dtable) + static_cast<long long>(token) * a.r + col;
+  const int cols = a.r - col;
+  float v[E];
+#pragma unroll
+  for (int j = 0; j < E; ++j) v[j] = s[j] * a.scale;
+  if (a.accumulate) {
+    if constexpr (kVec) {
+      if (lane * E < cols) Place<TO, true, E>::add(v, reinterpret_cast<const char*>(d), d, lane);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (lane + 32 * j < cols) v[j] += to_float(d[lane + 32 * j]);
+    }
+  }
+  save_lane<TO, kVec, E>(d, lane, cols, v);
+}
 
 template <typename TI, typename TO, bool kVec, bool kAdd>
 struct SumShared {

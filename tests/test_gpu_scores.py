@@ -393,3 +393,48 @@ def test_grad_sums_to_nothing_and_matches_differences():
             y[0, v] += step
             f.append(float(_run(y, t, 0)[0]["lp"].double()[0, 0]))
         assert abs((f[0] - f[1]) / (2 * h) - float(d[0, v])) < 4.1e-5 + 300 * U / (2 * h)
+
+
+@pytest.mark.parametrize("B,C", [(100, 5), (23, 17), (640, 4)])
+def test_logprobs_short_and_idle_requests(B, C):
+    """Requests of every length, idle ones among them (all their items left out), and a batch of nothing else."""
+    rng = np.random.default_rng(B)
+    x, held = _device_rows(_rows("plain", B * C, 700, rng), "f32", 4)
+    tokens = rng.integers(0, 700, size=(B, C)).astype(np.int32)
+    n_out = rng.integers(0, C + 1, size=B)
+    tokens[np.arange(C) >= n_out[:, None]] = -1
+    _check(x, held, tokens, 3)
+    _check(x, held, np.full_like(tokens, -1), 3)
+
+
+def test_calls_on_two_streams_at_once():
+    """Each stream with a workspace of its own; the same bits as one after the other."""
+    b = _binding()
+    V, r, n = 30000, 256, 6000
+    xs = [torch.randn(40, V, device="cuda") for _ in range(2)]
+    ts = [torch.randint(0, V, (40, 1), dtype=torch.int32, device="cuda") for _ in range(2)]
+    dout = [torch.randn(n, r, device="cuda") for _ in range(2)]
+    tok = [torch.randint(0, V // 50, (n,), dtype=torch.int32, device="cuda") for _ in range(2)]
+    want = [_run(x, t, 20)[0] for x, t in zip(xs, ts)]
+    size = b.dspark_embed_grad_workspace_bytes(n, V, r)
+    ws = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    grads = [torch.zeros(V, r, device="cuda") for _ in range(2)]
+    for k in range(2):
+        b.dspark_embed_grad(dout[k], tok[k], 0.5, grads[k], ws[k])
+    want_grads = [g.clone() for g in grads]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    for _ in range(10):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[k].append(_run(xs[k], ts[k], 20, ws=ws[k])[0])
+                grads[k].fill_(7.0)
+                b.dspark_embed_grad(dout[k], tok[k], 0.5, grads[k], ws[k])
+    torch.cuda.synchronize()
+    for k in range(2):
+        for o in outs[k]:
+            for name in o:
+                assert torch.equal(o[name], want[k][name])
+        assert torch.equal(grads[k], want_grads[k])
+        assert b.dspark_read_device_error(ws[k])[0] == 0
