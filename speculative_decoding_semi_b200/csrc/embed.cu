@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(2 * kSortThreads, 1) sort_kernel(GradArgs a) {
   }
   using Sorters = NamedSync<1, kSortThreads>;
   const unsigned lt = (1u << lane) - 1u;
-  for (int k = tid; k < W * R; k += nt) hist[k] = 0;
+  for (int k = tid; k < (W + 1) * R; k += nt) hist[k] = 0;      // and total
   Sorters::sync();
 
   // each warp's matches, in order: four neighbouring tokens a lane
@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(2 * kSortThreads, 1) sort_kernel(GradArgs a) {
         if (!hit[c]) continue;
         const unsigned off = static_cast<unsigned>(t[c] - v0);
         atomicAdd(count + off, 1u);
+        atomicAdd(total + off, 1u);
         if (at < a.keep) mine[at] = (static_cast<unsigned>(i + c - lo) << 11) | off;
         ++at;
       }
@@ -317,21 +318,15 @@ __global__ void __launch_bounds__(2 * kSortThreads, 1) sort_kernel(GradArgs a) {
   for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
   if (lane == 0 && below != 0u) atomicAdd(&s_below, below);
   Sorters::sync();
+  if (tid == 0) {                    // behind the barrier: every total is there
+    __threadfence_block();
+    s_counted = 1;
+  }
 
   // places: rows in order, within a row the warps in order
   const int per = ceil_div(rows, nt), r0 = min(rows, tid * per), r1 = min(rows, r0 + per);
   unsigned sum = 0;
-  for (int k = r0; k < r1; ++k) {
-    unsigned c = 0;
-#pragma unroll 8
-    for (int j = 0; j < W; ++j) {
-      const unsigned x = hist[j * R + k];
-      hist[j * R + k] = c;
-      c += x;
-    }
-    total[k] = c;
-    sum += c;
-  }
+  for (int k = r0; k < r1; ++k) sum += total[k];
   unsigned inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -340,18 +335,16 @@ __global__ void __launch_bounds__(2 * kSortThreads, 1) sort_kernel(GradArgs a) {
   }
   if (lane == 31) s_red[w] = inc;
   Sorters::sync();
-  if (tid == 0) {                    // behind the barrier: every total is there
-    __threadfence_block();
-    s_counted = 1;
-  }
   unsigned place = s_below + inc - sum;
   for (int j = 0; j < w; ++j) place += s_red[j];
   for (int k = r0; k < r1; ++k) {
     begin[k] = place;
-    if (total[k] != 0u) {
-#pragma unroll 8
-      for (int j = 0; j < W; ++j) hist[j * R + k] += place;
-      place += total[k];
+    if (total[k] == 0u) continue;          // most rows
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const unsigned x = hist[j * R + k];
+      hist[j * R + k] = place;
+      place += x;
     }
   }
   if (blockIdx.x == gridDim.x - 1 && tid == nt - 1) *a.n_sorted = static_cast<int>(place);
