@@ -3,11 +3,19 @@
 //
 // With m the row's largest logit, a row is reduced to
 //   S = sum 2^y,  T = sum y 2^y,  y = (x - m) log2 e,
-// so that ln p_v = x_v - m - ln S and the entropy is ln S - ln 2 T/S. The
-// difference x - m is taken before the product, so that masks of the type's
-// lowest value, and rows with nothing else, stay within range. Each lane
-// carries its own m, S and T through one pass over the row (a larger m scales
-// S and T) and the lanes' triples are joined at the end.
+// so that ln p_v = x_v - m - ln S and the entropy is ln S - ln 2 T/S. One pass
+// over the row: the sums are taken with the shift of a logit c near the
+// largest so far (a warp's first tile sets it, and it is raised only where
+// logits exceed it by more than kSlack), and moved to m at the end. Lanes each
+// raising their own c in every tile cost 9.4 instructions an element against
+// 7.8 so, and 228 us against 167 for 4,096 rows of 129,280 bf16.
+//
+// What bounds it: reading the rows. 4,096 x 129,280 bf16 takes 167 us, 6.3
+// TB/s (97% of the copy rate), and 197 us where the card's power cap holds the
+// SM clock at 1.67 GHz: bf16 rows need 70% of the exponential unit's rate at
+// full clock. 592 x 151,936 fp32: 56 us, 6.4 TB/s. Few rows are bound by
+// latency: 5.2 us for one row of 151,936 by a cluster of 8 CTAs, of which 3.0
+// remain with no tile to read; 20 alternatives add 5 us.
 #include <algorithm>
 
 #include "common.cuh"
@@ -360,6 +368,11 @@ __device__ int gathered_item(const int32_t* tokens, int items, int index, int* s
 // another holds an element in front of all of the other's. The pass over the
 // row notes the segments' maxima only; the chosen segments are read again for
 // the elements that reach the last one's maximum.
+//
+// A warp steps through tiles of 128 vectors, the next one in flight; 8 warps
+// and 64 registers let four CTAs share an SM (8 warps against 16, and 4 vectors
+// a lane against 8 without the next tile in flight: 171 against 198 us for the
+// bf16 rows above; two tiles in flight and three CTAs measured no faster).
 template <typename T, bool kTop>
 __global__ void __launch_bounds__(kMaxWarps * 32, 4) logprobs_kernel(ScoreArgs a) {
   constexpr int E = Vec<T>::kLen;
@@ -645,7 +658,10 @@ constexpr int kGradAhead = 4;
 // dlogits_v = p_v (c0 + c1 y_v) + g [v = t]: with y = (x - m) log2 e,
 // p = 2^y / s and ln p = y ln 2 - ln s, the bracket is
 // -g - g_H (ln p + H). Elementwise once the row's sums are known, so the row
-// is cut into pieces of kGradThreads * kGradAhead vectors, a CTA each.
+// is cut into pieces of kGradThreads * kGradAhead vectors, a CTA each, with
+// all of a thread's loads in flight before the row's scalars are read. Bound
+// by memory: 512 rows of 151,936 fp32 take 93 us, 6.7 TB/s read and written
+// (102% of the copy rate), 3,000 of 50,257 bf16 100 us, 6.0 TB/s.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(GradArgs a) {
   constexpr int E = Vec<T>::kLen;
