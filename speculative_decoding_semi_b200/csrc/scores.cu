@@ -293,7 +293,8 @@ __device__ __forceinline__ unsigned long long merge32(unsigned long long a, unsi
 // are merged in pairs. All warps of the CTA call; `out` is ready when they
 // return. Keys are different, or 0.
 template <typename Key>
-__device__ __forceinline__ void take_largest(int n, Key key, unsigned long long (*s_best)[32], unsigned long long* out) {
+__device__ __forceinline__ void take_largest(int n, Key key, unsigned long long (*s_best)[32],
+                                             unsigned long long* out) {
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, W = blockDim.x >> 5;
   const int busy = min(W, (n + 31) / 32);
   unsigned long long best = 0ull;
@@ -323,7 +324,9 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // Writes the first CTA's copy of a shared 64-bit word.
 __device__ __forceinline__ void write_first(const void* p, unsigned long long v) {
   unsigned a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(static_cast<unsigned>(__cvta_generic_to_shared(p))));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;"
+               : "=r"(a)
+               : "r"(static_cast<unsigned>(__cvta_generic_to_shared(p))));
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 
@@ -807,7 +810,8 @@ dspark_status dspark_logprobs(const void* logits, dspark_dtype dtype, int64_t n_
   ScoreArgs a{logits, n_rows, row_stride, row_start, tokens, C, V, top_k, logprob, entropy, stats, top_tokens,
               top_logprobs, reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + kErrOffset), 0, 1, 0, 1, 0};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == DSPARK_F32 ? launch_logprobs<float>(a, B * C, s) : launch_logprobs<uint16_t>(a, B * C, s);
+  const cudaError_t e =
+      dtype == DSPARK_F32 ? launch_logprobs<float>(a, B * C, s) : launch_logprobs<uint16_t>(a, B * C, s);
   return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
