@@ -253,7 +253,8 @@ dspark_status dspark_advance_anchor(const int32_t* out_tokens, const int32_t* n_
  * used for its error word (except by dspark_embed_grad): any initialised
  * workspace of dspark_workspace_bytes serves. A token id below -1 or >= V, or
  * a row outside [0, n_rows), is recorded there (detail 0x7.......: the item)
- * and the item treated as left out.
+ * and the item treated as left out. The first call on a device may load the
+ * library's device code, so make it before any stream capture.
  */
 
 /*

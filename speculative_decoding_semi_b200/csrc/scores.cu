@@ -801,6 +801,7 @@ dspark_status dspark_logprobs(const void* logits, dspark_dtype dtype, int64_t n_
   if (dtype != DSPARK_F32 && dtype != DSPARK_BF16) return DSPARK_ERR_INVALID_ARG;
   if (B < 0 || C < 0 || static_cast<long long>(B) * C > kMaxItems || V < 1 || V > kMaxV) return DSPARK_ERR_INVALID_ARG;
   if (n_rows < 0 || n_rows > kMaxStride || row_stride < V || row_stride > kMaxStride) return DSPARK_ERR_INVALID_ARG;
+  if (n_rows > (1ll << 60) / row_stride) return DSPARK_ERR_INVALID_ARG;
   if (top_k < 0 || top_k > DSPARK_MAX_TOP_K) return DSPARK_ERR_INVALID_ARG;
   if (B == 0 || C == 0) return DSPARK_OK;
   if (!given(logits) || !given(tokens) || !given(logprob) || !given(workspace)) return DSPARK_ERR_INVALID_ARG;

@@ -77,7 +77,7 @@ def _logprobs(lib, **kw):
     dict(logits=None), dict(logits=FAKE + 4), dict(tokens=None), dict(tokens=FAKE + 4), dict(logprob=None),
     dict(entropy=FAKE + 4), dict(stats=FAKE + 8), dict(row_start=FAKE + 8), dict(top=None), dict(top_lp=None),
     dict(ws=None), dict(ws_bytes=16), dict(dtype=2), dict(dtype=-1), dict(B=-1), dict(C=-1), dict(V=0),
-    dict(V=(1 << 24) + 1, stride=1 << 25), dict(stride=999), dict(stride=1 << 33), dict(n_rows=-1), dict(k=33),
+    dict(V=(1 << 24) + 1, stride=1 << 25), dict(stride=999), dict(stride=1 << 33), dict(n_rows=-1), dict(n_rows=1 << 32, stride=1 << 32), dict(k=33),
     dict(k=-1), dict(B=1 << 13, C=(1 << 11) + 1)])
 def test_logprobs_refuses(lib, bad):
     assert _logprobs(lib, **bad) == INVALID
