@@ -4,31 +4,12 @@
 // another (token, row; sorted order, row, parts).
 #include <algorithm>
 
-#include "common.cuh"
+#include "elements.cuh"
 
 namespace dspark {
 namespace {
 
-constexpr int kMaxItems = 1 << 24;
-constexpr int kMaxSms = 148;   // owners of table rows, one CTA each (more only for very large V)
-
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(uint16_t x) { return bf16_bits_to_float(x); }
-
-// Two fp32 values as a pair of bf16, rounded to nearest even.
-__device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
-  unsigned r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ void store(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store(uint16_t* p, float v) { *p = static_cast<uint16_t>(pack_bf16(v, 0.f)); }
-
-__device__ __forceinline__ void record_bad_token(unsigned* err, int item) {
-  set_error(err, DSPARK_ERR_DEVICE_ASSERT, 0x70000000u | static_cast<unsigned>(item));
-}
 
 // ---------------------------------------------------------------- lookup
 
@@ -111,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a) {
     const int i = i0 + u * blockDim.y;
     t[u] = i < a.n ? __ldg(a.tokens + i) : -1;
     if (t[u] < -1 || t[u] >= a.V) {
-      if (threadIdx.x == 0) record_bad_token(a.err, i);
+      if (threadIdx.x == 0) record_bad_item(a.err, i);
       t[u] = -1;
     }
   }
@@ -156,7 +137,7 @@ cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t s) {
   const dim3 block(x, kThreads / x);
   // two rows a thread once that fills the GPU (60,000 rows of 256, bf16 to
   // fp32: one 20.9 us, two 16.3, four 18.2, eight 18.8)
-  const int rows = static_cast<long long>(a.n) >= 8ll * kMaxSms * block.y ? 2 : 1;
+  const int rows = static_cast<long long>(a.n) >= 8ll * kSms * block.y ? 2 : 1;
   const int grid = ceil_div(a.n, static_cast<int>(block.y) * rows);
   auto kernel = vec ? (rows == 2 ? embed_kernel<TI, TO, true, 2> : embed_kernel<TI, TO, true, 1>)
                     : (rows == 2 ? embed_kernel<TI, TO, false, 2> : embed_kernel<TI, TO, false, 1>);
@@ -187,8 +168,8 @@ cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t s) {
 //
 // Measured: 512 rows of 256 fp32 added to a gradient 3.7 us (direct), written
 // whole into 151,936 rows 26.6 (zeroing alone 24); 10,007 of 200 bf16 into
-// 50,257 fp32 rows 17.8 (sort beside zeroing 10, sums 10, joins 4, starts
-// overlapped); 65,536 of 1,024 bf16 into 129,280 88 (45, 36, 6). An owner that
+// 50,257 fp32 rows 16.9 (sort beside zeroing 10, sums 8.5, joins 4, starts
+// overlapped); 65,536 of 1,024 bf16 into 129,280 86 (45, 33, 6). An owner that
 // summed its own rows as well took twice as long: one CTA an SM has too few
 // loads in flight. Joining through counters in the sums' kernel cost as much
 // as the third kernel, since a release waits for the SM's stores. Zeroing what
@@ -307,7 +288,7 @@ __global__ void __launch_bounds__(2 * kSortThreads, 1) sort_kernel(GradArgs a) {
       }
       if (blockIdx.x == 0)
         for (int c = 0; c < 4; ++c)
-          if (t[c] < -1 || t[c] >= a.V) record_bad_token(a.err, i + c);
+          if (t[c] < -1 || t[c] >= a.V) record_bad_item(a.err, i + c);
       if (__ballot_sync(0xffffffffu, any) == 0u) continue;
       int at = found;
 #pragma unroll
@@ -609,9 +590,7 @@ __global__ void __launch_bounds__(kSumThreads, kAdd ? 2 : 5) sum_kernel(GradArgs
   };
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) fetch(u, u);
-  int u = 0;
-#pragma unroll 1
-  for (int j = 0; j < items; ++j) {
+  auto take = [&](int j, int u) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
     if (!kVec) __syncwarp();      // the other lanes' copies
     Place<TI, kVec, E>::add(sum, sh.rows[w][u],
@@ -636,7 +615,14 @@ __global__ void __launch_bounds__(kSumThreads, kAdd ? 2 : 5) sum_kernel(GradArgs
     }
     if (!kVec) __syncwarp();      // the place is read
     fetch(j + kAhead, u);
-    u = u == kAhead - 1 ? 0 : u + 1;
+  };
+  // unrolled over the ring, so that its places are constants (88 -> 86 us for
+  // the 65,536 rows above)
+#pragma unroll 1
+  for (int j0 = 0; j0 < items; j0 += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (j0 + u < items) take(j0 + u, u);
   }
   if (!__syncthreads_or((ends & ~shorts) != 0u)) return;
   // The first part of a run here is one that starts in a window, or comes into
@@ -764,7 +750,7 @@ __global__ void __launch_bounds__(kDirectThreads) direct_kernel(GradArgs a) {
   }
   const int t = __ldg(a.tokens + i);
   if (t < 0 || t >= a.V) {
-    if (t != -1 && tid == 0 && blockIdx.y == 0) record_bad_token(a.err, i);
+    if (t != -1 && tid == 0 && blockIdx.y == 0) record_bad_item(a.err, i);
     zeroed();
     return;
   }
@@ -840,7 +826,7 @@ struct GradPlan {
 GradPlan grad_plan(int n, int V, int r, int lane_cols) {
   constexpr int kSmemWords = (224 << 10) / 4;
   GradPlan p{};
-  p.R = std::min(kMaxR, ceil_div(V, kMaxSms));
+  p.R = std::min(kMaxR, ceil_div(V, kSms));     // one owner an SM, more for very large V
   p.owners = ceil_div(V, p.R);
   p.keep = std::min((kSmemWords - 256 - (kSortWarps + 2) * p.R) / kSortWarps, std::max(32, ceil_div(n, kSortWarps)));
   p.slabs = ceil_div(r, 32 * lane_cols);
@@ -853,9 +839,6 @@ GradPlan grad_plan(int n, int V, int r, int lane_cols) {
   return p;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool given(const void* p) { return p != nullptr && aligned16(p); }
-bool dtype_ok(dspark_dtype t) { return t == DSPARK_F32 || t == DSPARK_BF16; }
 bool embed_sizes_ok(int n, int V, int r) {
   return n >= 0 && n <= kMaxItems && V >= 1 && V <= kMaxV && r >= 1 && r <= DSPARK_MAX_EMBED_R;
 }
@@ -883,7 +866,7 @@ cudaError_t launch_grad(GradArgs a, char* ws, cudaStream_t s) {
       char* d = static_cast<char*>(a.dtable);
       const long long vecs = bytes / 16;
       const long long blocks = (vecs + kZeroThreads - 1) / kZeroThreads;
-      const int grid = static_cast<int>(std::max(1ll, std::min<long long>(2 * kMaxSms, blocks)));
+      const int grid = static_cast<int>(std::max(1ll, std::min<long long>(2 * kSms, blocks)));
       zero_kernel<<<grid, kZeroThreads, 0, s>>>(reinterpret_cast<uint4*>(d), vecs,
                                                 reinterpret_cast<uint16_t*>(d + vecs * 16),
                                                 static_cast<int>(bytes - vecs * 16) / 2);
@@ -939,9 +922,9 @@ extern "C" {
 dspark_status dspark_embed(const void* table, dspark_dtype table_dtype, const int32_t* tokens, int n, int V, int r,
                            float scale, void* out, dspark_dtype out_dtype, void* workspace, size_t ws_bytes,
                            dspark_stream_t stream) {
-  if (!dtype_ok(table_dtype) || !dtype_ok(out_dtype) || !embed_sizes_ok(n, V, r)) return DSPARK_ERR_INVALID_ARG;
+  if (!is_element_type(table_dtype) || !is_element_type(out_dtype) || !embed_sizes_ok(n, V, r)) return DSPARK_ERR_INVALID_ARG;
   if (n == 0) return DSPARK_OK;
-  if (!given(table) || !given(tokens) || !given(out) || !given(workspace)) return DSPARK_ERR_INVALID_ARG;
+  if (!is_given(table) || !is_given(tokens) || !is_given(out) || !is_given(workspace)) return DSPARK_ERR_INVALID_ARG;
   if (ws_bytes < kScratchOffset) return DSPARK_ERR_INVALID_ARG;
   const EmbedArgs a{table, tokens, n, V, r, scale, out,
                     reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + kErrOffset)};
@@ -961,10 +944,10 @@ size_t dspark_embed_grad_workspace_bytes(int n, int V, int r) {
 dspark_status dspark_embed_grad(const void* dout, dspark_dtype dout_dtype, const int32_t* tokens, int n, int V, int r,
                                 float scale, int accumulate, void* dtable, dspark_dtype dtable_dtype,
                                 void* workspace, size_t ws_bytes, dspark_stream_t stream) {
-  if (!dtype_ok(dout_dtype) || !dtype_ok(dtable_dtype) || !embed_sizes_ok(n, V, r)) return DSPARK_ERR_INVALID_ARG;
+  if (!is_element_type(dout_dtype) || !is_element_type(dtable_dtype) || !embed_sizes_ok(n, V, r)) return DSPARK_ERR_INVALID_ARG;
   if (accumulate != 0 && accumulate != 1) return DSPARK_ERR_INVALID_ARG;
-  if (!given(dtable) || !given(workspace)) return DSPARK_ERR_INVALID_ARG;
-  if (n > 0 && (!given(dout) || !given(tokens))) return DSPARK_ERR_INVALID_ARG;
+  if (!is_given(dtable) || !is_given(workspace)) return DSPARK_ERR_INVALID_ARG;
+  if (n > 0 && (!is_given(dout) || !is_given(tokens))) return DSPARK_ERR_INVALID_ARG;
   if (ws_bytes < dspark_embed_grad_workspace_bytes(n, V, r)) return DSPARK_ERR_INVALID_ARG;
   GradArgs a{};
   a.dout = dout;

@@ -18,16 +18,14 @@
 // remain with no tile to read; 20 alternatives add 5 us.
 #include <algorithm>
 
-#include "common.cuh"
+#include "elements.cuh"
 
 namespace dspark {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr double kLn2 = 0.69314718055994530942;
-constexpr int kMaxItems = 1 << 24;
 constexpr long long kMaxStride = 1ll << 32;
-constexpr int kSms = 148;
 // exponents below this give 2^y = 0; the clamp keeps y 2^y from being -inf * 0
 constexpr float kMinExp = -16384.f;
 
@@ -63,18 +61,6 @@ struct GradArgs {
   unsigned* err;
   int pieces;  // CTAs of a row
 };
-
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(uint16_t x) { return bf16_bits_to_float(x); }
-
-// Two fp32 values as a pair of bf16, rounded to nearest even.
-__device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
-  unsigned r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ void store(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store(uint16_t* p, float v) { *p = static_cast<uint16_t>(pack_bf16(v, 0.f)); }
 
 // 2^y, relative error below 2^-22; results below 2^-126 are 0.
 __device__ __forceinline__ float ex2(float y) {
@@ -399,7 +385,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4) logprobs_kernel(ScoreArgs a
   bool skip = tok == -1;
   const long long row = a.row_start != nullptr ? a.row_start[b] + (item - b * a.C) : static_cast<long long>(item);
   if (!skip && (tok < 0 || tok >= V || row < 0 || row >= a.n_rows)) {
-    if (tid == 0 && part == 0) set_error(a.err, DSPARK_ERR_DEVICE_ASSERT, 0x70000000u | static_cast<unsigned>(item));
+    if (tid == 0 && part == 0) record_bad_item(a.err, item);
     skip = true;
   }
   if (skip) {                       // the same for every CTA of the cluster
@@ -684,7 +670,7 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(GradArgs a)
   const float2 st = reinterpret_cast<const float2*>(a.stats)[row];
   const float g = a.g_logprob[row];
   if (tid == 0 && piece == 0 && (tok < -1 || tok >= V))
-    set_error(a.err, DSPARK_ERR_DEVICE_ASSERT, 0x70000000u | static_cast<unsigned>(row));
+    record_bad_item(a.err, row);
   const bool none = tok < 0 || tok >= V || st.x == -INFINITY;
   const float f = 1.f / st.y, lf = -logf(st.y);
   float c0 = -g, c1 = 0.f;
@@ -730,8 +716,6 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(GradArgs a)
   }
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool given(const void* p) { return p != nullptr && aligned16(p); }
 
 template <typename T>
 cudaError_t launch_logprobs(ScoreArgs a, int items, cudaStream_t s) {
@@ -798,15 +782,15 @@ dspark_status dspark_logprobs(const void* logits, dspark_dtype dtype, int64_t n_
                               const int64_t* row_start, const int32_t* tokens, int B, int C, int V, int top_k,
                               float* logprob, float* entropy, float* stats, int32_t* top_tokens,
                               float* top_logprobs, void* workspace, size_t ws_bytes, dspark_stream_t stream) {
-  if (dtype != DSPARK_F32 && dtype != DSPARK_BF16) return DSPARK_ERR_INVALID_ARG;
+  if (!is_element_type(dtype)) return DSPARK_ERR_INVALID_ARG;
   if (B < 0 || C < 0 || static_cast<long long>(B) * C > kMaxItems || V < 1 || V > kMaxV) return DSPARK_ERR_INVALID_ARG;
   if (n_rows < 0 || n_rows > kMaxStride || row_stride < V || row_stride > kMaxStride) return DSPARK_ERR_INVALID_ARG;
   if (n_rows > (1ll << 60) / row_stride) return DSPARK_ERR_INVALID_ARG;
   if (top_k < 0 || top_k > DSPARK_MAX_TOP_K) return DSPARK_ERR_INVALID_ARG;
   if (B == 0 || C == 0) return DSPARK_OK;
-  if (!given(logits) || !given(tokens) || !given(logprob) || !given(workspace)) return DSPARK_ERR_INVALID_ARG;
-  if (!aligned16(row_start) || !aligned16(entropy) || !aligned16(stats)) return DSPARK_ERR_INVALID_ARG;
-  if (top_k > 0 && (!given(top_tokens) || !given(top_logprobs))) return DSPARK_ERR_INVALID_ARG;
+  if (!is_given(logits) || !is_given(tokens) || !is_given(logprob) || !is_given(workspace)) return DSPARK_ERR_INVALID_ARG;
+  if (!is_aligned16(row_start) || !is_aligned16(entropy) || !is_aligned16(stats)) return DSPARK_ERR_INVALID_ARG;
+  if (top_k > 0 && (!is_given(top_tokens) || !is_given(top_logprobs))) return DSPARK_ERR_INVALID_ARG;
   if (ws_bytes < kScratchOffset) return DSPARK_ERR_INVALID_ARG;
   ScoreArgs a{logits, n_rows, row_stride, row_start, tokens, C, V, top_k, logprob, entropy, stats, top_tokens,
               top_logprobs, reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + kErrOffset), 0, 1, 0, 1, 0};
@@ -820,14 +804,14 @@ dspark_status dspark_logprobs_grad(const void* logits, dspark_dtype dtype, int64
                                    const int32_t* tokens, const float* stats, const float* entropy,
                                    const float* g_logprob, const float* g_entropy, int N, int V, void* dlogits,
                                    int64_t grad_stride, void* workspace, size_t ws_bytes, dspark_stream_t stream) {
-  if (dtype != DSPARK_F32 && dtype != DSPARK_BF16) return DSPARK_ERR_INVALID_ARG;
+  if (!is_element_type(dtype)) return DSPARK_ERR_INVALID_ARG;
   if (N < 0 || N > kMaxItems || V < 1 || V > kMaxV) return DSPARK_ERR_INVALID_ARG;
   if (row_stride < V || row_stride > kMaxStride || grad_stride < V || grad_stride > kMaxStride)
     return DSPARK_ERR_INVALID_ARG;
   if (N == 0) return DSPARK_OK;
-  if (!given(logits) || !given(tokens) || !given(stats) || !given(g_logprob) || !given(dlogits) || !given(workspace))
+  if (!is_given(logits) || !is_given(tokens) || !is_given(stats) || !is_given(g_logprob) || !is_given(dlogits) || !is_given(workspace))
     return DSPARK_ERR_INVALID_ARG;
-  if (g_entropy != nullptr && (!given(g_entropy) || !given(entropy))) return DSPARK_ERR_INVALID_ARG;
+  if (g_entropy != nullptr && (!is_given(g_entropy) || !is_given(entropy))) return DSPARK_ERR_INVALID_ARG;
   if (dlogits == logits && row_stride != grad_stride) return DSPARK_ERR_INVALID_ARG;
   if (ws_bytes < kScratchOffset) return DSPARK_ERR_INVALID_ARG;
   GradArgs a{logits, row_stride, grad_stride, tokens, stats, entropy, g_logprob, g_entropy, V, dlogits,
