@@ -163,7 +163,7 @@ cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t s) {
 //   shared memory, and those of a run that goes on go to scratch.
 // join_kernel: adds the CTAs' parts of each such run in order.
 //
-// Few items: direct_kernel, one CTA an item, no sorting; without accumulate it
+// Few items: direct_kernel, one CTA an item and up to 8 slabs, no sorting; without accumulate it
 // runs beside zero_kernel and waits for it before it writes.
 //
 // Measured: 512 rows of 256 fp32 added to a gradient 3.7 us (direct), written
@@ -185,6 +185,7 @@ struct GradArgs {
   void* dtable;
   unsigned* err;
   int R, slabs, pieces;   // table rows of an owner; slabs of a row; pieces (a CTA's windows) of the sorted items
+  int direct;             // slabs of a CTA of the direct path
   int keep;               // matches that a warp of the sort keeps in shared memory; more are found again
   int* n_sorted;          // items with a token
   int4* sorted;           // [n] item, token, and the run [begin, end) it is in
@@ -197,7 +198,7 @@ constexpr int kWindow = 16;     // sorted items of a warp
 constexpr int kShort = 16;      // a run up to this length belongs to one warp (kWindow + kShort <= 32)
 constexpr int kAhead = 6;       // rows of a warp in flight
 constexpr int kSumWarps = 8, kSumThreads = kSumWarps * 32, kPiece = kSumWarps * kWindow;
-constexpr int kDirectItems = 4096, kDirectAlways = 512, kDirectWork = 5120;   // items; items; items times slabs
+constexpr int kDirectItems = 4096, kDirectAlways = 512, kDirectWork = 6144;   // items; items; items times slabs
 constexpr int kDirectWarps = 8, kDirectThreads = kDirectWarps * 32;
 
 template <typename TO>
@@ -787,9 +788,9 @@ __global__ void __launch_bounds__(kDirectThreads) direct_kernel(GradArgs a) {
       for (unsigned m = word[u]; m != 0u; m &= m - 1)
         s_items[at++] = static_cast<short>((lane * kWords + u) * 32 + __ffs(m) - 1);
   __syncthreads();
-  const int here = min(kDirectWarps, a.slabs - static_cast<int>(blockIdx.y) * kDirectWarps);   // slabs of this CTA
+  const int slab0 = static_cast<int>(blockIdx.y) * a.direct, here = min(a.direct, a.slabs - slab0);
   const int groups = kDirectWarps / here;
-  const int group = w / here, col = (static_cast<int>(blockIdx.y) * kDirectWarps + w % here) * kSlab<TI>;
+  const int group = w / here, col = (slab0 + w % here) * kSlab<TI>;
   float sum[E];
   clear(sum);
   if (group < groups) {
@@ -856,9 +857,10 @@ cudaError_t launch_grad(GradArgs a, char* ws, cudaStream_t s) {
   cfg.numAttrs = a.accumulate ? 0 : 1;
   // Each CTA of the direct path reads all tokens, and its 8 warps share a
   // frequent token's items only as far as the slabs leave warps for it
-  // (accumulating rows of fp32, direct against sorted: 1,500 x 256 6.6 us
-  // against 11.7, 2,379 x 64 8.3 against 11.8, 4,000 x 256 13.1 against 12.4,
-  // 2,379 x 1,024 28.6 against 13.6).
+  // (accumulating rows of fp32, direct against sorted: 1,500 x 256 7.1 us
+  // against 11.9, 3,000 x 256 11.7 against 12.4, 750 x 1,024 8.3 against 11.5,
+  // 4,000 x 64 13.5 against 13.2, 4,000 x 256 14.2 against 12.9, 2,379 x 1,024
+  // 23.4 against 12.6).
   if (a.n <= kDirectAlways ||
       (a.n <= kDirectItems && static_cast<long long>(a.n) * a.slabs <= kDirectWork)) {
     if (!a.accumulate) {
@@ -874,7 +876,12 @@ cudaError_t launch_grad(GradArgs a, char* ws, cudaStream_t s) {
       if (e != cudaSuccess) return e;
     }
     if (a.n == 0) return cudaSuccess;
-    cfg.gridDim = dim3(a.n, ceil_div(a.slabs, kDirectWarps));
+    // Fewer slabs a CTA leave more of its warps for a frequent token's items,
+    // but more CTAs read the tokens (8, 4 and 2 a CTA: 600 x 384 6.4 us, 6.5,
+    // 5.3; 1,200 x 512 9.2, 9.2, 9.8; 600 x 1,024 10.7, 7.9, 8.1; 512 x 2,048
+    // 10.4, 9.1, 11.3; 300 x 8,192 12.2, 14.6, 22.1).
+    a.direct = a.slabs <= 4 && a.n <= 1024 ? 2 : a.slabs <= 16 ? 4 : kDirectWarps;
+    cfg.gridDim = dim3(a.n, ceil_div(a.slabs, a.direct));
     cfg.blockDim = dim3(kDirectThreads);
     return cudaLaunchKernelEx(&cfg, a.n <= 1024 ? direct_kernel<TI, TO, kVec, 1024> : direct_kernel<TI, TO, kVec, 4096>,
                               a);

@@ -143,6 +143,15 @@ def test_embed_grad_distributions(kind, n, V, r, accumulate):
 
 
 @pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("kind", ["same", "zipf"])
+@pytest.mark.parametrize("n,V,r", [(900, 50, 515), (1024, 3000, 500), (1025, 200, 500), (512, 40, 2050), (256, 30, 2052)])
+def test_embed_grad_slabs(kind, n, V, r, accumulate):
+    """Rows that several CTAs share, the last with a part of its slabs."""
+    _check_grad(kind, n, V, r, "f32", "f32", accumulate)
+    _check_grad(kind, n, V, r, "bf16", "bf16", accumulate, seed=1)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
 def test_embed_grad_large(accumulate):
     _check_grad("zipf", 100003, 30011, 24, "f32", "f32", accumulate)
     _check_grad("zipf", 66000, 129280, 64, "bf16", "f32", accumulate)
