@@ -824,8 +824,9 @@ struct GradPlan {
   int R, owners, keep, slabs, pieces;
   size_t smem, off_n, off_sorted, off_parts, bytes;
 };
+constexpr int kSortSmem = 224 << 10;    // what an owner's words of any plan fit in
 GradPlan grad_plan(int n, int V, int r, int lane_cols) {
-  constexpr int kSmemWords = (224 << 10) / 4;
+  constexpr int kSmemWords = kSortSmem / 4;
   GradPlan p{};
   p.R = std::min(kMaxR, ceil_div(V, kSms));     // one owner an SM, more for very large V
   p.owners = ceil_div(V, p.R);
@@ -892,8 +893,10 @@ cudaError_t launch_grad(GradArgs a, char* ws, cudaStream_t s) {
   a.n_sorted = reinterpret_cast<int*>(ws + p.off_n);
   a.sorted = reinterpret_cast<int4*>(ws + p.off_sorted);
   a.parts = reinterpret_cast<float*>(ws + p.off_parts);
-  cudaError_t e = cudaFuncSetAttribute(sort_kernel<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(p.smem));
+  // The limit is the function's, on the device, for all host threads: one that
+  // went by this call's sizes could be lowered by another thread before the
+  // launch below.
+  cudaError_t e = cudaFuncSetAttribute(sort_kernel<TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
   if (e != cudaSuccess) return e;
   sort_kernel<TO><<<p.owners, (a.accumulate ? 1 : 2) * kSortThreads, p.smem, s>>>(a);
   e = cudaGetLastError();
