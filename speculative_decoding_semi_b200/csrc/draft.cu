@@ -136,7 +136,10 @@ cudaError_t launch_draft_generic(DraftArgs a, int G, cudaStream_t stream) {
   const size_t smem = static_cast<size_t>(RB) * a.r * sizeof(float);
   void* fn = a.bf16 ? reinterpret_cast<void*>(&draft_generic_kernel<true>)
                     : reinterpret_cast<void*>(&draft_generic_kernel<false>);
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // what the largest rank needs: the limit is the function's, for all host
+  // threads, and must not go by the sizes of one call
+  constexpr int kLimit = RB * kMaxR * static_cast<int>(sizeof(float));
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kLimit);
   if (e != cudaSuccess) return e;
   int per_sm = 0;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, DT, smem);

@@ -1088,7 +1088,9 @@ cudaError_t launch_draft_tc(DraftArgs a, int G, unsigned* sync, char* extra, cud
       draft_tc_kernel<true, true, false>,   draft_tc_kernel<true, true, true>};
   const void* fn = reinterpret_cast<const void*>(
       kernels[(a.W != nullptr ? 4 : 0) + (store_z ? 2 : 0) + (p.spread ? 1 : 0)]);
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // the limit is the function's, for all host threads: not by the sizes of one
+  // call (the kernel has no static shared memory)
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
   if (e != cudaSuccess) return e;
   int per_sm = 0;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kThreads, smem);

@@ -574,10 +574,13 @@ cudaError_t launch_residual_tc(const Params& P, cudaStream_t stream) {
   cudaDeviceGetAttribute(&max_smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int choices[][2] = {{4, 3}, {4, 2}, {3, 2}, {2, 2}};
+  // the limit is the function's, for all host threads: not by the sizes of one
+  // call; 1 KB is left for the kernel's static shared memory (16 bytes)
+  const int limit = max_smem - 1024;
   size_t smem = 0;
   for (const auto& c : choices) {
     const size_t need = rs_layout(c[0], rp.gsize, a.r, c[1]).total + 1024;
-    if (static_cast<int>(need) <= max_smem) {
+    if (static_cast<int>(need) <= limit) {
       rp.nbf = c[0];
       rp.nbs = c[1];
       smem = need;
@@ -587,7 +590,7 @@ cudaError_t launch_residual_tc(const Params& P, cudaStream_t stream) {
   if (smem == 0) return cudaErrorInvalidConfiguration;
   CUtensorMap tm_bf;
   if (!encode_bf_tiles(&tm_bf, a.Bf, a.V, a.r)) return cudaErrorInvalidValue;
-  e = cudaFuncSetAttribute(residual_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  e = cudaFuncSetAttribute(residual_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
   if (e != cudaSuccess) return e;
   const int G = std::max(1, std::min(std::min(kMaxGrid, sms), a.V / kUnit));
   cudaLaunchConfig_t cfg{};

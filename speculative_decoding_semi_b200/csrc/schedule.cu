@@ -223,7 +223,10 @@ cudaError_t launch_schedule(ScheduleArgs a, char* scratch, cudaStream_t stream) 
   const int ST = big ? 1024 : 256;
   const void* fn = big ? reinterpret_cast<const void*>(&schedule_kernel<1024>)
                        : reinterpret_cast<const void*>(&schedule_kernel<256>);
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // what the most items need: the limit is the function's, for all host
+  // threads, and must not go by the sizes of one call
+  constexpr int kLimit = kMaxScheduleItems * static_cast<int>(sizeof(double));
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kLimit);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);

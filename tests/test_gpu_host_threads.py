@@ -56,3 +56,32 @@ def test_embed_grad_of_different_sizes(accumulate):
     for got, want, ws in checks:
         assert b.dspark_read_device_error(ws)[0] == 0
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("sizes", [((512, 32), (64, 32)), ((200, 8), (3, 5))])
+def test_schedule_of_different_sizes(sizes):
+    """Both kernels (2,048 items and more, and fewer), each with two sizes of shared memory."""
+    from speculative_decoding_semi_b200 import binding as b
+    calls, checks = [], []
+    for B, K in sizes * 3:
+        gen = torch.Generator(device="cuda").manual_seed(B)
+        conf, temps = torch.randn(B, K, device="cuda", generator=gen), torch.ones(K, device="cuda")
+        profile = 1.0 + 0.01 * torch.arange(B * (K + 1) + 1, dtype=torch.float32, device="cuda")
+        i32 = torch.int32
+        outs = (torch.empty(B, dtype=i32, device="cuda"), torch.empty(B, K, device="cuda"),
+                torch.empty(B, dtype=torch.int64, device="cuda"), torch.empty(1, dtype=i32, device="cuda"))
+        ws = torch.zeros(b.dspark_workspace_bytes(B, K, 8, 1), dtype=torch.uint8, device="cuda")
+        stream = torch.cuda.Stream()
+        b.dspark_schedule(conf, temps, profile, *outs, ws)
+        torch.cuda.synchronize()
+        want = [o.clone() for o in outs]
+        for o in outs:
+            o.zero_()
+        calls.append(lambda a=(conf, temps, profile, *outs, ws), s=stream: b.dspark_schedule(*a, s))
+        checks.append((outs, want, ws))
+    torch.cuda.synchronize()
+    _at_once(calls, 2000)
+    for outs, want, ws in checks:
+        assert b.dspark_read_device_error(ws)[0] == 0
+        for got, w in zip(outs, want):
+            assert torch.equal(got, w)
