@@ -40,6 +40,16 @@ class HeadGradients:
         dspark_workspace_init(self.workspace)
 
 
+def _torch_stream(stream, device) -> torch.cuda.Stream:
+    """What the entry points take as `stream` (None: the current one, a torch stream, or a handle; 0 is the legacy
+    default stream) as a torch stream."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if not isinstance(stream, int):
+        return stream
+    return torch.cuda.ExternalStream(stream, device=device) if stream != 0 else torch.cuda.default_stream(device)
+
+
 def head_gradients(d: dict, bufs: RoundBuffers, grads: HeadGradients, anchor=None, entropy_bonus: float = 0.0,
                    accumulate: bool = False, stream=None) -> torch.Tensor:
     """The loss (a device scalar), with its gradients in grads.dA and grads.dBf
@@ -54,7 +64,7 @@ def head_gradients(d: dict, bufs: RoundBuffers, grads: HeadGradients, anchor=Non
     B, K, V, r = grads.B, grads.K, grads.V, grads.r
     if (bufs.B, bufs.K, bufs.V, bufs.r) != (B, K, V, r):
         raise ValueError(f"a round of {(bufs.B, bufs.K, bufs.V, bufs.r)} for gradients of {(B, K, V, r)}")
-    with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(grads.dA.device)):
+    with torch.cuda.stream(_torch_stream(stream, grads.dA.device)):
         labels = bufs.out_tokens[:, :K].contiguous()
         used = labels >= 0
         n = used.sum().clamp(min=1)

@@ -188,3 +188,23 @@ def test_round_scores_and_gradients_in_one_graph():
     assert torch.equal(got[1], scores.logprob) and torch.equal(got[2], scores.top_tokens)
     # drows is a library product, whose order may differ between capture and eager: V half steps of its magnitudes
     assert float((got[3] - grads.dA).abs().max()) <= bufs.V * U * float(grads.dA.abs().max() + 1)
+
+
+@pytest.mark.parametrize("legacy", [False, True])
+def test_head_gradients_on_a_stream_handle(legacy):
+    """`stream` as the integer handle that the entry points take; 0 is the legacy default stream."""
+    from speculative_decoding_semi_b200 import head, round as rnd
+    inp, d, bufs = _round()
+    rnd.run_round(d, bufs)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    grads = head.HeadGradients(bufs.B, bufs.K, bufs.V, bufs.r)
+    torch.cuda.synchronize()
+    before = torch.cuda.current_stream()
+    loss = head.head_gradients(d, bufs, grads, stream=0 if legacy else s.cuda_stream)
+    (torch.cuda.default_stream() if legacy else s).synchronize()
+    assert torch.cuda.current_stream() == before
+    want, dA, dBf, mA, mB = _reference(inp, bufs, 0.0)
+    assert abs(float(loss) - want) <= 400 * U * (1 + abs(want))
+    for got, ref, mag in ((grads.dA, dA, mA), (grads.dBf, dBf, mB)):
+        assert bool(((got.double().cpu() - ref).abs() <= (bufs.V + 400) * U * mag + 1e-30).all())
