@@ -222,3 +222,22 @@ def test_embed_grad_captured_and_on_a_side_stream(n):
         torch.cuda.current_stream().wait_stream(s)
         assert torch.equal(a, want) and torch.equal(c, total)
     assert b.dspark_read_device_error(ws)[0] == 0
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embed_grad_of_the_most_items(accumulate):
+    """2^24 items of three tokens and some left out, where an item's place and its token's row fill the sort's words;
+    sums of whole numbers below 2^24 are exact in any order."""
+    b = _binding()
+    n, V = 1 << 24, 4
+    i = torch.arange(n, dtype=torch.int32, device="cuda")
+    tokens = (i % 3).int()
+    tokens[::1001] = -1
+    dout = (1 + (i & 1)).float()[:, None]
+    dtable = torch.full((V, 1), 5.0, device="cuda")
+    ws = _ws(n, V, 1)
+    b.dspark_embed_grad(dout, tokens, 1.0, dtable, ws, accumulate=accumulate)
+    assert b.dspark_read_device_error(ws)[0] == 0
+    want = torch.zeros(V + 1, 1, dtype=torch.float64, device="cuda").index_add_(0, tokens.long() + 1, dout.double())[1:]
+    assert float(want.max()) < 1 << 24
+    assert torch.equal(dtable.double(), want + (5.0 if accumulate else 0.0))

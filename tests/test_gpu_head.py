@@ -208,3 +208,38 @@ def test_head_gradients_on_a_stream_handle(legacy):
     assert abs(float(loss) - want) <= 400 * U * (1 + abs(want))
     for got, ref, mag in ((grads.dA, dA, mA), (grads.dBf, dBf, mB)):
         assert bool(((got.double().cpu() - ref).abs() <= (bufs.V + 400) * U * mag + 1e-30).all())
+
+
+def test_replayed_scores_and_gradients_match_the_definition():
+    """The captured step on other inputs: its gradients by the bounds of an eager step (sums of magnitudes of each
+    entry), its scores bit by bit."""
+    from speculative_decoding_semi_b200 import head, round as rnd
+    _, d, bufs = _round(seed=41)
+    scores, grads = rnd.TokenScores(bufs.B, bufs.K, top_k=4), head.HeadGradients(bufs.B, bufs.K, bufs.V, bufs.r)
+
+    def step():
+        rnd.run_round(d, bufs, scores=scores)
+        return head.head_gradients(d, bufs, grads, entropy_bonus=0.1)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        loss = step()
+    inp, other, _ = _round(seed=42)
+    for name, t in d.items():
+        t.copy_(other[name])
+    g.replay()
+    torch.cuda.synchronize()
+    want, dA, dBf, mA, mB = _reference(inp, bufs, 0.1)
+    assert abs(float(loss) - want) <= 400 * U * (1 + abs(want))
+    for got, ref, mag in ((grads.dA, dA, mA), (grads.dBf, dBf, mB)):
+        assert bool(((got.double().cpu() - ref).abs() <= (bufs.V + 400) * U * mag + 1e-30).all())
+    replayed = {n: getattr(scores, n).clone() for n in ("logprob", "entropy", "stats", "top_tokens", "top_logprobs")}
+    step()
+    torch.cuda.synchronize()
+    for n, t in replayed.items():
+        assert torch.equal(t, getattr(scores, n)), n

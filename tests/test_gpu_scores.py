@@ -438,3 +438,46 @@ def test_calls_on_two_streams_at_once():
                 assert torch.equal(o[name], want[k][name])
         assert torch.equal(grads[k], want_grads[k])
         assert b.dspark_read_device_error(ws[k])[0] == 0
+
+
+def _short_requests(B, C, V, rng):
+    """Tokens [B,C] of requests of every length, idle ones among them, and where their packed rows start."""
+    n_out = rng.integers(0, C + 1, size=B)
+    n_out[:3] = 0, C, 2
+    tokens = rng.integers(0, V, size=(B, C)).astype(np.int32)
+    tokens[np.arange(C) >= n_out[:, None]] = -1
+    return tokens, (np.cumsum(n_out) - n_out).astype(np.int64), int(n_out.sum())
+
+
+@pytest.mark.parametrize("dtype,B,C,V", [("f32", 20, 5, 40000), ("bf16", 20, 5, 40001), ("f32", 64, 9, 16397)])
+@pytest.mark.parametrize("k", [0, 20])
+def test_logprobs_short_requests_of_long_rows(dtype, B, C, V, k):
+    """Requests of several lengths whose rows are long enough to be shared by the CTAs of a cluster."""
+    rng = np.random.default_rng(B + V)
+    tokens, start, rows = _short_requests(B, C, V, rng)
+    x, held = _device_rows(_rows("plain", rows, V, rng), dtype, 1)
+    _check(x, held, tokens, k, row_start=start)
+
+
+@pytest.mark.parametrize("dtype,V", [("f32", 40000), ("bf16", 40001)])
+def test_logprobs_errors_among_long_rows(dtype, V):
+    """A bad token, and a request whose second row lies behind the last: recorded (one of the two), treated as left
+    out, and the other items are scored as without them."""
+    b = _binding()
+    rng = np.random.default_rng(V)
+    B, C, k = 20, 5, 20
+    tokens, start, rows = _short_requests(B, C, V, rng)
+    x, held = _device_rows(_rows("plain", rows, V, rng), dtype, 0)
+    tokens[1, 3] = V
+    start[2] = rows - 1
+    outs, ws = _run(x, torch.from_numpy(tokens).cuda(), k, row_start=torch.from_numpy(start).cuda())
+    code, detail = b.dspark_read_device_error(ws)
+    assert code == 5 and detail in (0x70000000 | (C + 3), 0x70000000 | (2 * C + 1))
+    o = _host(outs)
+    for i in range(B):
+        for c in range(C):
+            if tokens[i, c] < 0 or (i, c) in ((1, 3), (2, 1)):
+                assert o["lp"][i, c] == 0 and o["H"][i, c] == 0 and np.all(o["st"][i, c] == 0)
+                assert np.all(o["top"][i, c] == -1) and np.all(o["tlp"][i, c] == -np.inf)
+            else:
+                _check_item(o, (i, c), scores.row_scores(held[start[i] + c], tokens[i, c], k), k)
