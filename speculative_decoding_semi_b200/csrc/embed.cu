@@ -910,7 +910,7 @@ cudaError_t launch_grad(GradArgs a, char* ws, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = cudaLaunchKernelEx(&cfg, sum, a);
   if (e != cudaSuccess) return e;
-  if (a.n <= kPiece) return cudaSuccess;
+  static_assert(kDirectAlways >= kPiece, "the sorted path has more than one piece");
   cfg.gridDim = dim3(ceil_div(p.pieces, kJoinWarps) * p.slabs);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
