@@ -20,6 +20,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import statistics
 import sys
 import threading
@@ -215,15 +216,26 @@ def cpu_baseline(inp: dict, seconds: float = 15.0, single_thread_seconds: float 
     return out
 
 
+# the translation units of the kernels whose DRAM traffic is recorded (and the ABI that picks them)
+TRAFFIC_SOURCES = ("api.cu", "draft_tc.cu", "verify.cu")
+
+
 def source_digest() -> str:
-    """sha256 over the library's CUDA sources: a recorded DRAM traffic figure is
-    only reported while the kernels are the ones it was measured on."""
-    h = hashlib.sha256()
+    """sha256 over the CUDA sources of the recorded kernels and the library's
+    files that they include: a recorded DRAM traffic figure is only reported
+    while the kernels are the ones it was measured on."""
     src = os.path.join(ROOT, "speculative_decoding_semi_b200", "csrc")
-    for name in sorted(os.listdir(src)):
-        if name.endswith((".cu", ".cuh", ".h")):
-            with open(os.path.join(src, name), "rb") as f:
-                h.update(name.encode() + b"\0" + f.read())
+    texts, todo = {}, list(TRAFFIC_SOURCES)
+    while todo:
+        name = todo.pop()
+        if name in texts:
+            continue
+        with open(os.path.join(src, name), "rb") as f:
+            texts[name] = f.read()
+        todo += [m.decode() for m in re.findall(rb'^#include "([^"/]+)"', texts[name], re.M)]
+    h = hashlib.sha256()
+    for name in sorted(texts):
+        h.update(name.encode() + b"\0" + texts[name])
     return h.hexdigest()
 
 

@@ -1,5 +1,7 @@
 """bench.py's measurement arithmetic on the host (no GPU)."""
 import json
+import os
+import shutil
 
 import numpy as np
 import pytest
@@ -60,3 +62,19 @@ def test_traffic_reported_only_for_the_captured_sources(tmp_path, monkeypatch):
 def test_source_digest_covers_the_kernels():
     d1 = bench.source_digest()
     assert len(d1) == 64 and d1 == bench.source_digest()
+
+
+def test_source_digest_goes_by_what_the_recorded_kernels_include(tmp_path, monkeypatch):
+    src = os.path.join(bench.ROOT, "speculative_decoding_semi_b200", "csrc")
+    copy = tmp_path / "speculative_decoding_semi_b200" / "csrc"
+    shutil.copytree(src, copy)
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    before = bench.source_digest()
+    for name, same in (("embed.cu", True), ("elements.cuh", True), ("schedule.cu", True), ("draft_tc.cu", False),
+                       ("verify.cu", False), ("verify_common.cuh", False), ("sm100.cuh", False),
+                       ("common.cuh", False), ("kernels.h", False)):
+        text = (copy / name).read_text()
+        (copy / name).write_text(text + "// one more line\n")
+        assert (bench.source_digest() == before) == same, name
+        (copy / name).write_text(text)
+    assert bench.source_digest() == before
