@@ -246,10 +246,11 @@ dspark_status dspark_advance_anchor(const int32_t* out_tokens, const int32_t* n_
  * either; [QbitAI] section "online drafter calibration" (the drafter corrects
  * itself from the workload it sees) is their place in the method.
  *
- * These entry points take any V from 1 to 2^24 (no multiple of 8), rows of
- * logits `row_stride` >= V elements apart (so that rows need not be 16-byte
- * aligned; the base pointers are), and zero items (DSPARK_OK, nothing is
- * launched). A token id of -1 marks an item to leave out. The workspace is
+ * These entry points take any V from 1 to 2^24 (V need not be a multiple of
+ * 8), rows of logits `row_stride` >= V elements apart (so that rows need not
+ * be 16-byte aligned; the base pointers are), and zero items (DSPARK_OK;
+ * nothing is launched, except that dspark_embed_grad with accumulate = 0
+ * zeroes the table). A token id of -1 marks an item to leave out. The workspace is
  * used for its error word (except by dspark_embed_grad): any initialised
  * workspace of dspark_workspace_bytes serves. A token id below -1 or >= V, or
  * a row outside [0, n_rows), is recorded there (detail 0x7.......: the item)
@@ -281,7 +282,10 @@ dspark_status dspark_advance_anchor(const int32_t* out_tokens, const int32_t* n_
  * -1 and -inf where a row has fewer than top_k unmasked tokens. An item left
  * out gets 0 in logprob, entropy and stats, -1 and -inf as alternatives, and
  * its row is not read. Sums are taken in fp32 over at most 64 terms at a time
- * and beyond that in fp64, in an order that depends on the sizes only.
+ * and beyond that in fp64, in an order that depends on the sizes, on where the
+ * row starts between 16-byte boundaries and on its values: the same call on
+ * the same rows gives the same bits, the same logits at another row may differ
+ * in the last ones.
  */
 #define DSPARK_MAX_TOP_K 32
 dspark_status dspark_logprobs(const void* logits, dspark_dtype dtype, int64_t n_rows, int64_t row_stride,
