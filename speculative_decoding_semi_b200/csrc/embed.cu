@@ -81,7 +81,10 @@ __device__ __forceinline__ void save_cols(uint16_t* p, const float (&v)[N]) {
 // blockDim.x threads a row (kCols columns each, or single ones where r is no
 // multiple of kCols), blockDim.y * kRows rows a CTA, kRows of them in flight a
 // thread. 16,384 rows of 4,096, bf16 to fp32: 55 us, 6.0 TB/s with each table
-// row read once (92% of the copy rate); 64 rows of 256: 1.4 us.
+// row read once (92% of the copy rate); 64 rows of 256: 1.4 us. Single columns
+// are loads and stores of 2 or 4 bytes, bound by their number: 16,384 distinct
+// rows, bf16 to fp32, of 4,096 columns 67 us and of 4,095 110, of 1,000 20 and
+// of 1,001 32 (bf16 to bf16 14 and 30, fp32 to fp32 24 and 35).
 template <typename TI, typename TO, bool kVec, int kRows>
 __global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a) {
   constexpr int N = kVec ? kCols<TI, TO> : 1;
@@ -173,8 +176,9 @@ cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t s) {
 // summed its own rows as well took twice as long: one CTA an SM has too few
 // loads in flight. Joining through counters in the sums' kernel cost as much
 // as the third kernel, since a release waits for the SM's stores. Zeroing what
-// is left beside the sums, and two slabs a warp, gained nothing: the sums issue
-// 73% of the slots they have at four CTAs an SM.
+// is left beside the sums, and two slabs a warp, gained nothing for the last of
+// these, where memory is busy anyway and the sums issue 73% of the slots they
+// have at four CTAs an SM; smaller ones were not tried.
 
 struct GradArgs {
   const void* dout;

@@ -722,7 +722,9 @@ cudaError_t launch_logprobs(ScoreArgs a, int items, cudaStream_t s) {
   constexpr int E = Vec<T>::kLen;
   const int tiles = std::max(1, (a.V / E + kTile - 1) / kTile);
   // rows to read, as far as can be told here: a round's emitted tokens fill
-  // about half of its items or less
+  // about half of its items or less. Where nearly all drafts are accepted there
+  // are up to twice as many, and a row may get more CTAs than is best for them
+  // (the 366 rows below)
   const long long rows = a.C > 1 ? (items + 1) / 2 : items;
   // few rows: a row is shared by the CTAs of a cluster, while that leaves each
   // eight tiles or more. Two CTAs up to four an SM; four and eight, whose

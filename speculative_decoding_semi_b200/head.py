@@ -5,7 +5,8 @@ calibration": the drafter corrects itself from the workload it sees. Where
 dspark_calibrate moves the confidence temperatures, this moves the head: the
 emitted tokens are the labels of the draft's positions. Position i of request b
 has one if the drafts before it were all accepted (out_tokens[b,i] for
-i < n_out[b]: an accepted draft, or the token drawn at the first rejection), and
+i < n_out[b]: an accepted draft, the token drawn at the first rejection, or the
+bonus token where the verify length ends before K), and
   loss = -(1/n) sum log q_i(label) - (entropy_bonus/n) sum H(q_i)
 over the n positions that have one, q_i = softmax(z_i), z_i = base_i + A[t_{i-1}] . Bf.
 The log probabilities, their gradient dz, the rows of A and the gradient of A

@@ -156,7 +156,9 @@ def run_rounds(inputs: list, bufs: RoundBuffers, state: RoundState, rounds: int,
     and the anchors and temperatures in `state`, which the round updates.
     calibrate = (eta, t_min, t_max) turns on the online temperature step.
     With record=True each round's state and outputs are copied into history
-    tensors [rounds, ...] (device-to-device). With graph=True the rounds are
+    tensors [rounds, ...] (device-to-device). Tokens are not scored here: each
+    round overwrites out_tokens; run_round and `score` score a round's tokens
+    before the next. With graph=True the rounds are
     captured once as a CUDA graph and replayed; the graph is returned in the
     result under "graph" so that it can be replayed again.
     """
